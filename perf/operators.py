@@ -82,7 +82,8 @@ def draw(rng):
     if op == "tables":
         lo = _log_int(rng, 8, 20000)
         return {"op": op, "B": _log_int(rng, 1, 500), "s_q": rng.randint(1, 8), "cached_min": lo,
-                "cached_max": lo + rng.randint(0, 10000), "new_min": rng.randint(0, 1), "new_max": _log_int(rng, 1, 4000), "heads": heads}
+                "cached_max": lo + rng.randint(0, 10000), "new_min": rng.randint(0, 1),
+                "new_max": _log_int(rng, 1, 4000), "heads": heads}
     if op == "append":
         n = _log_int(rng, 1, 16384)
         return {"op": op, "n": n, "blocks": rng.randint(256, 4096), "pad": rng.choice([0, rng.randint(1, 100)])}
