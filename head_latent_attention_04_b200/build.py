@@ -18,7 +18,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmla.so")
-SOURCES = ["capi.cu", "plan.cpp", "head_gemm.cu", "decode_attn.cu", "combine.cu", "noalloc.cu", "prefill.cu", "upstream.cu"]
+SOURCES = ["capi.cu", "plan.cpp", "head_gemm.cu", "decode_attn.cu", "combine.cu", "noalloc.cu", "prefill.cu", "upstream.cu",
+           "cache_fp4.cu", "decode_attn_fp4.cu", "tables.cu", "pages.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -310,6 +310,152 @@ mla_status_t mla_kv_quantize_fp8(const void* kv, const int32_t* slots, int64_t n
   return launch_kv_quantize_fp8(kv, slots, n, pool_fp8, (long long)num_blocks * 64, status, stream);
 }
 
+static mla_status_t check_words(const void* p, const char* name) {   // int32 and fp32 arrays
+  if (!p) return set_error(MLA_ERR_INVALID_ARG, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(p) & 3u) return set_error(MLA_ERR_INVALID_ARG, "%s is not 4-byte aligned", name);
+  return MLA_OK;
+}
+
+static mla_status_t check_optional_words(const void* p, const char* name) { return p ? check_words(p, name) : MLA_OK; }
+
+static mla_status_t check_pool(int64_t n, int32_t num_blocks) {
+  if (n < 0 || num_blocks < 1) return set_error(MLA_ERR_INVALID_ARG, "n must be >= 0 and num_blocks >= 1");
+  if ((int64_t)num_blocks * 64 > INT32_MAX) return set_error(MLA_ERR_UNSUPPORTED, "pool too large");
+  return MLA_OK;
+}
+
+mla_status_t mla_kv_quantize_fp4(const void* kv, const int32_t* slots, int64_t n, void* pool_fp4,
+                                 int32_t num_blocks, int32_t* status, void* stream) {
+  clear_error();
+  MLA_TRY(check_pool(n, num_blocks));
+  if (n == 0) return MLA_OK;
+  MLA_TRY(check_ptr(kv, "kv"));
+  MLA_TRY(check_words(slots, "slots"));
+  MLA_TRY(check_ptr(pool_fp4, "pool_fp4"));
+  MLA_TRY(check_optional_words(status, "status"));
+  return launch_kv_quantize_fp4(kv, slots, n, pool_fp4, (long long)num_blocks * 64, status, stream);
+}
+
+mla_status_t mla_kv_dequantize_fp4(const void* pool_fp4, const int32_t* slots, int64_t n, void* kv,
+                                   int32_t num_blocks, int32_t* status, void* stream) {
+  clear_error();
+  MLA_TRY(check_pool(n, num_blocks));
+  if (n == 0) return MLA_OK;
+  MLA_TRY(check_ptr(pool_fp4, "pool_fp4"));
+  MLA_TRY(check_words(slots, "slots"));
+  MLA_TRY(check_ptr(kv, "kv"));
+  MLA_TRY(check_optional_words(status, "status"));
+  return launch_kv_dequantize_fp4(pool_fp4, slots, n, kv, (long long)num_blocks * 64, status, stream);
+}
+
+mla_status_t mla_decode_attn_fp4cache(const mla_dims_t* dims, const void* q_lat, const void* q_rope,
+                                      const void* kv_pool_fp4, const int32_t* block_table,
+                                      const int32_t* seq_lens, const void* plan_dev, int32_t num_clusters,
+                                      float* o_part, float* lse_part, void* o_lat, float* lse_out,
+                                      int32_t* status, void* stream) {
+  clear_error();
+  MLA_TRY(check_dims(dims));
+  MLA_TRY(check_ptr(q_lat, "q_lat"));
+  MLA_TRY(check_ptr(q_rope, "q_rope"));
+  MLA_TRY(check_ptr(kv_pool_fp4, "kv_pool_fp4"));
+  MLA_TRY(check_words(block_table, "block_table"));
+  MLA_TRY(check_words(seq_lens, "seq_lens"));
+  MLA_TRY(check_words(plan_dev, "plan_dev"));
+  MLA_TRY(check_ptr(o_lat, "o_lat"));
+  MLA_TRY(check_optional_words(lse_out, "lse_out"));
+  MLA_TRY(check_optional_words(status, "status"));
+  if (num_clusters < 1 || num_clusters > 4096)
+    return set_error(MLA_ERR_INVALID_ARG, "num_clusters must be in [1, 4096]");
+  if ((o_part && (reinterpret_cast<uintptr_t>(o_part) & 31u)) || (lse_part && (reinterpret_cast<uintptr_t>(lse_part) & 3u)))
+    return set_error(MLA_ERR_INVALID_ARG, "o_part must be 32-byte aligned, lse_part 4-byte aligned");
+  return launch_decode_attn_fp4cache(*dims, q_lat, q_rope, kv_pool_fp4, block_table, seq_lens,
+                                     static_cast<const int32_t*>(plan_dev), num_clusters, o_part, lse_part,
+                                     o_lat, lse_out, status, stream);
+}
+
+mla_status_t mla_build_tables(int32_t B, const int32_t* cached_lens, const int32_t* new_lens,
+                              int32_t max_blocks_per_seq, int32_t* block_table, const int32_t* free_blocks,
+                              int32_t n_free, const int32_t* free_head, int32_t num_blocks, int32_t max_new,
+                              int32_t* seq_lens, int32_t* cu_new, int32_t* slots, int32_t* positions,
+                              int32_t* free_head_out, int32_t* status, void* stream) {
+  clear_error();
+  if (B < 1 || max_blocks_per_seq < 1 || n_free < 0 || num_blocks < 1 || max_new < 0)
+    return set_error(MLA_ERR_INVALID_ARG, "B, max_blocks_per_seq and num_blocks must be >= 1, n_free and max_new >= 0");
+  if (B > 65536) return set_error(MLA_ERR_UNSUPPORTED, "more than 65536 requests");
+  if ((int64_t)max_blocks_per_seq * 64 > INT32_MAX - 64 || (int64_t)num_blocks * 64 > INT32_MAX)
+    return set_error(MLA_ERR_UNSUPPORTED, "max_blocks_per_seq or num_blocks too large");
+  MLA_TRY(check_words(cached_lens, "cached_lens"));
+  MLA_TRY(check_words(new_lens, "new_lens"));
+  MLA_TRY(check_words(block_table, "block_table"));
+  if (n_free > 0) MLA_TRY(check_words(free_blocks, "free_blocks"));
+  MLA_TRY(check_words(free_head, "free_head"));
+  MLA_TRY(check_words(seq_lens, "seq_lens"));
+  MLA_TRY(check_words(cu_new, "cu_new"));
+  if (max_new > 0) MLA_TRY(check_words(slots, "slots"));
+  MLA_TRY(check_optional_words(positions, "positions"));
+  MLA_TRY(check_words(free_head_out, "free_head_out"));
+  MLA_TRY(check_optional_words(status, "status"));
+  return launch_build_tables(B, cached_lens, new_lens, max_blocks_per_seq, block_table, free_blocks, n_free, free_head,
+                             num_blocks, max_new, seq_lens, cu_new, slots, positions, free_head_out, status, stream);
+}
+
+mla_status_t mla_plan_device(const mla_dims_t* dims, const int32_t* seq_lens, int32_t num_clusters, void* plan_dev,
+                             size_t plan_bytes, int32_t* status, void* stream) {
+  clear_error();
+  MLA_TRY(check_dims(dims));
+  if (num_clusters < 1 || num_clusters > 4096)
+    return set_error(MLA_ERR_INVALID_ARG, "num_clusters must be in [1, 4096]");
+  if ((int64_t)dims->max_blocks_per_seq * 64 > INT32_MAX - 64)
+    return set_error(MLA_ERR_UNSUPPORTED, "max_blocks_per_seq too large");
+  MLA_TRY(check_words(seq_lens, "seq_lens"));
+  MLA_TRY(check_words(plan_dev, "plan_dev"));
+  MLA_TRY(check_optional_words(status, "status"));
+  if (plan_bytes < (size_t)plan_words_upper_bound(num_clusters, dims->B * dims->s_q) * 4)
+    return set_error(MLA_ERR_WORKSPACE_TOO_SMALL, "plan buffer smaller than mla_plan_size");
+  return launch_plan(*dims, seq_lens, num_clusters, static_cast<int32_t*>(plan_dev), status, stream);
+}
+
+mla_status_t mla_summarize_pages(const void* kv_pool, int32_t cache, const int32_t* blocks, int32_t n,
+                                 int32_t num_blocks, void* codes, float* scales, int32_t* status, void* stream) {
+  clear_error();
+  if (cache != MLA_CACHE_BF16 && cache != MLA_CACHE_FP8 && cache != MLA_CACHE_FP4)
+    return set_error(MLA_ERR_INVALID_ARG, "cache must be MLA_CACHE_BF16, MLA_CACHE_FP8 or MLA_CACHE_FP4");
+  MLA_TRY(check_pool(n, num_blocks));
+  if (n == 0) return MLA_OK;
+  MLA_TRY(check_ptr(kv_pool, "kv_pool"));
+  MLA_TRY(check_words(blocks, "blocks"));
+  MLA_TRY(check_ptr(codes, "codes"));
+  MLA_TRY(check_words(scales, "scales"));
+  MLA_TRY(check_optional_words(status, "status"));
+  return launch_summarize_pages(kv_pool, cache, blocks, n, num_blocks, codes, scales, status, stream);
+}
+
+mla_status_t mla_select_pages(const mla_dims_t* dims, const void* q_lat, const void* q_rope, const void* codes,
+                              const float* scales, const int32_t* block_table, const int32_t* seq_lens, int32_t k,
+                              int32_t n_first, int32_t n_recent, float* scores, int32_t* sel_table,
+                              int32_t* sel_lens, int32_t* sel_pages, int32_t* status, void* stream) {
+  clear_error();
+  MLA_TRY(check_dims(dims));
+  if ((int64_t)dims->max_blocks_per_seq * 64 > INT32_MAX - 64)
+    return set_error(MLA_ERR_UNSUPPORTED, "max_blocks_per_seq too large");
+  if (n_first < 0 || n_recent < 1 || k < 1 || (int64_t)n_first + n_recent > k)
+    return set_error(MLA_ERR_INVALID_ARG, "n_first >= 0, n_recent >= 1 and n_first + n_recent <= k are needed");
+  if ((int64_t)k * 64 > INT32_MAX - 64) return set_error(MLA_ERR_UNSUPPORTED, "k too large");
+  MLA_TRY(check_ptr(q_lat, "q_lat"));
+  MLA_TRY(check_ptr(q_rope, "q_rope"));
+  MLA_TRY(check_ptr(codes, "codes"));
+  MLA_TRY(check_words(scales, "scales"));
+  MLA_TRY(check_words(block_table, "block_table"));
+  MLA_TRY(check_words(seq_lens, "seq_lens"));
+  MLA_TRY(check_words(scores, "scores"));
+  MLA_TRY(check_words(sel_table, "sel_table"));
+  MLA_TRY(check_words(sel_lens, "sel_lens"));
+  MLA_TRY(check_optional_words(sel_pages, "sel_pages"));
+  MLA_TRY(check_optional_words(status, "status"));
+  return launch_select_pages(*dims, q_lat, q_rope, codes, scales, block_table, seq_lens, k, n_first, n_recent, scores,
+                             sel_table, sel_lens, sel_pages, status, stream);
+}
+
 mla_status_t mla_combine(const mla_dims_t* dims, const void* plan_dev, const float* o_part,
                          const float* lse_part, void* o_lat, float* lse_out, void* stream) {
   clear_error();
@@ -408,7 +554,10 @@ mla_status_t mla_prefill_attn(const void* q_nope, const void* q_rope, const void
                              lse, stream);
 }
 
-void mla_set_wait_limit_ns(int64_t ns) { set_decode_wait_limit_ns(ns); }
+void mla_set_wait_limit_ns(int64_t ns) {
+  set_decode_wait_limit_ns(ns);
+  set_decode_fp4_wait_limit_ns(ns);
+}
 
 mla_status_t mla_debug_gather_pages(const void* kv_pool, const int32_t* block_table, int32_t b,
                                     int32_t n_pages, int32_t max_blocks_per_seq, int32_t num_blocks,

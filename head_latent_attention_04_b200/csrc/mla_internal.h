@@ -64,6 +64,30 @@ mla_status_t launch_decode_attn_fp8cache(const mla_dims_t& d, const void* q_lat,
 // bf16 cache rows [n][576] -> FP8 pool slots (flat token index block * 64 + row).
 mla_status_t launch_kv_quantize_fp8(const void* kv, const int32_t* slots, long long n, void* pool_fp8,
                                    long long pool_rows, int32_t* status, void* stream);
+// bf16 cache rows -> 4-bit pool slots, and 4-bit pool slots -> bf16 rows (slot -1: padding, skipped).
+mla_status_t launch_kv_quantize_fp4(const void* kv, const int32_t* slots, long long n, void* pool_fp4,
+                                    long long pool_rows, int32_t* status, void* stream);
+mla_status_t launch_kv_dequantize_fp4(const void* pool_fp4, const int32_t* slots, long long n, void* out,
+                                      long long pool_rows, int32_t* status, void* stream);
+mla_status_t launch_decode_attn_fp4cache(const mla_dims_t& d, const void* q_lat, const void* q_rope,
+                                         const void* kv_pool_fp4, const int32_t* block_table,
+                                         const int32_t* seq_lens, const int32_t* plan_dev, int32_t num_clusters,
+                                         float* o_part, float* lse_part, void* o_lat, float* lse_out,
+                                         int32_t* status, void* stream);
+void set_decode_fp4_wait_limit_ns(int64_t ns);
+mla_status_t launch_build_tables(int B, const int32_t* cached_lens, const int32_t* new_lens, int max_blocks,
+                                 int32_t* block_table, const int32_t* free_blocks, int n_free,
+                                 const int32_t* free_head, int num_blocks, int max_new, int32_t* seq_lens,
+                                 int32_t* cu_new, int32_t* slots, int32_t* positions, int32_t* free_head_out,
+                                 int32_t* status, void* stream);
+mla_status_t launch_plan(const mla_dims_t& d, const int32_t* seq_lens, int num_clusters, int32_t* plan,
+                         int32_t* status, void* stream);
+mla_status_t launch_summarize_pages(const void* kv_pool, int kind, const int32_t* blocks, int n, int num_blocks,
+                                    void* codes, float* scales, int32_t* status, void* stream);
+mla_status_t launch_select_pages(const mla_dims_t& d, const void* q_lat, const void* q_rope, const void* codes,
+                                 const float* scales, const int32_t* block_table, const int32_t* seq_lens, int k,
+                                 int n_first, int n_recent, float* scores, int32_t* sel_table, int32_t* sel_lens,
+                                 int32_t* sel_pages, int32_t* status, void* stream);
 mla_status_t launch_combine(const mla_dims_t& d, const int32_t* plan_dev, int32_t n_rows,
                             const float* o_part, const float* lse_part, void* o_lat,
                             float* lse_out, void* stream);

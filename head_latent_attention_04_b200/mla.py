@@ -7,6 +7,7 @@ shared library has not been built: there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -24,14 +25,16 @@ _lib = ctypes.CDLL(_LIB_PATH)
 MLA_OK, MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED = 0, 1, 2
 MLA_ERR_WORKSPACE_TOO_SMALL, MLA_ERR_CUDA, MLA_ERR_TIMEOUT = 3, 4, 5
 STATUS_BAD_BLOCK, STATUS_TIMEOUT, STATUS_BAD_SEQLEN, STATUS_BAD_PLAN, STATUS_SCORE_RANGE = 0x1, 0x2, 0x4, 0x8, 0x10
-STATUS_CACHE_RANGE = 0x20
+STATUS_CACHE_RANGE, STATUS_NO_SPACE = 0x20, 0x40
+CACHE_KINDS = {"bf16": 0, "fp8": 1, "fp4": 2}
 EXPORTS = ("mla_version", "mla_last_error_string", "mla_absorb_q", "mla_out_uv",
            "mla_max_clusters", "mla_plan_size", "mla_plan", "mla_decode_attn", "mla_combine",
            "mla_debug_gather_pages", "mla_decode_attn_combine_noalloc", "mla_noalloc_scratch_bytes",
            "mla_quantize_w_uk_fp8", "mla_quantize_w_uv_fp8", "mla_quantize_rows_fp8", "mla_absorb_q_fp8",
            "mla_out_uv_fp8", "mla_set_wait_limit_ns", "mla_decode_attn_tree", "mla_prefill_up_proj",
            "mla_prefill_attn", "mla_qkv_a_proj", "mla_q_up_absorb", "mla_decode_attn_fp8cache",
-           "mla_kv_quantize_fp8")
+           "mla_kv_quantize_fp8", "mla_kv_quantize_fp4", "mla_kv_dequantize_fp4", "mla_decode_attn_fp4cache",
+           "mla_build_tables", "mla_plan_device", "mla_summarize_pages", "mla_select_pages")
 
 
 class MlaDims(ctypes.Structure):
@@ -56,6 +59,13 @@ for _name, _args in {
     "mla_decode_attn_tree": [_pdims, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp],
     "mla_decode_attn_fp8cache": [_pdims, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp],
     "mla_kv_quantize_fp8": [_vp, _vp, ctypes.c_int64, _vp, _i32, _vp, _vp],
+    "mla_kv_quantize_fp4": [_vp, _vp, ctypes.c_int64, _vp, _i32, _vp, _vp],
+    "mla_kv_dequantize_fp4": [_vp, _vp, ctypes.c_int64, _vp, _i32, _vp, _vp],
+    "mla_decode_attn_fp4cache": [_pdims, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp],
+    "mla_build_tables": [_i32, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+    "mla_plan_device": [_pdims, _vp, _i32, _vp, _sz, _vp, _vp],
+    "mla_summarize_pages": [_vp, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp],
+    "mla_select_pages": [_pdims, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp],
     "mla_combine": [_pdims, _vp, _vp, _vp, _vp, _vp, _vp],
     "mla_debug_gather_pages": [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp],
     "mla_decode_attn_combine_noalloc": [_pdims, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i32, _vp, _vp, _vp, _vp],
@@ -104,6 +114,34 @@ def _ptr(t) -> int | None:
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor (the library assumes row-major layouts)")
     return t.data_ptr()
+
+
+def _arg(t, name: str, dtype, *shape) -> int | None:
+    """Device address of a tensor argument of the given type and shape (a None
+    extent takes any), refused here when it is anything else."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if len(shape) != t.dim() or any(w is not None and w != h for w, h in zip(shape, t.shape)):
+        want = ", ".join("*" if w is None else str(w) for w in shape)
+        raise ValueError(f"{name}: expected shape [{want}], got {list(t.shape)}")
+    return _ptr(t)
+
+
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _on(first, *others):
+    """The device of the tensors of one call, made current for the launch (a
+    launch goes to the current device, and its default stream is that device's)."""
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors of one call on {dev} and {t.device}")
+    if not first.is_cuda:
+        raise ValueError(f"expected a CUDA tensor, got one on {dev}")
+    return _SAME_DEVICE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _stream(stream=None) -> int:
@@ -274,6 +312,152 @@ def fp8_pool_from(kv_pool, stream=None):
     return kv_quantize_fp8(kv_pool.reshape(nb * 64, 576), slots, pool8, stream=stream)
 
 
+FP4_ROW_BYTES = 416   # 256 bytes of E2M1 codes | 16 fp16 group scales | 64 bf16 k_rope
+
+
+def decode_attn_fp4cache(dims, q_lat, q_rope, kv_pool_fp4, block_table, seq_lens, plan_dev, num_clusters,
+                         o_part, lse_part, o_lat, lse_out=None, status=None, stream=None):
+    """decode_attn on a 4-bit latent cache: ``kv_pool_fp4`` uint8
+    [num_blocks][64][416] as :func:`kv_quantize_fp4` writes it."""
+    N, H = dims.B * dims.s_q, dims.n_heads
+    with _on(q_lat, q_rope, kv_pool_fp4, block_table, seq_lens, plan_dev, o_part, lse_part, o_lat, lse_out, status):
+        _check(_lib.mla_decode_attn_fp4cache(
+            ctypes.byref(dims), _arg(q_lat, "q_lat", torch.bfloat16, N, H, 512),
+            _arg(q_rope, "q_rope", torch.bfloat16, N, H, 64),
+            _arg(kv_pool_fp4, "kv_pool_fp4", torch.uint8, dims.num_blocks, 64, FP4_ROW_BYTES),
+            _arg(block_table, "block_table", torch.int32, dims.B, dims.max_blocks_per_seq),
+            _arg(seq_lens, "seq_lens", torch.int32, dims.B), _arg(plan_dev, "plan_dev", torch.int32, None),
+            num_clusters, _ptr(o_part), _ptr(lse_part), _arg(o_lat, "o_lat", torch.bfloat16, N, H, 512),
+            _arg(lse_out, "lse_out", torch.float32, N, H), _ptr(status), _stream(stream)), "mla_decode_attn_fp4cache")
+
+
+def kv_quantize_fp4(kv, slots, kv_pool_fp4, status=None, stream=None):
+    """bf16 cache rows ``kv`` [n][576] -> slots ``slots`` (int32 [n], block * 64 +
+    row; -1 is padding) of the 4-bit pool (uint8 [num_blocks][64][416])."""
+    n = slots.shape[0]
+    with _on(kv_pool_fp4, kv, slots, status):
+        _check(_lib.mla_kv_quantize_fp4(_arg(kv, "kv", torch.bfloat16, n, 576), _arg(slots, "slots", torch.int32, n), n,
+                                        _arg(kv_pool_fp4, "kv_pool_fp4", torch.uint8, None, 64, FP4_ROW_BYTES),
+                                        kv_pool_fp4.shape[0], _ptr(status), _stream(stream)), "mla_kv_quantize_fp4")
+    return kv_pool_fp4
+
+
+def kv_dequantize_fp4(kv_pool_fp4, slots, kv=None, status=None, stream=None):
+    """Slots of a 4-bit pool -> bf16 rows ``kv`` [n][576] (rows of padding and of
+    bad slots are left as they were; zeros when ``kv`` is made here)."""
+    n = slots.shape[0]
+    if kv is None:
+        kv = torch.zeros((n, 576), dtype=torch.bfloat16, device=kv_pool_fp4.device)
+    with _on(kv_pool_fp4, kv, slots, status):
+        _check(_lib.mla_kv_dequantize_fp4(_arg(kv_pool_fp4, "kv_pool_fp4", torch.uint8, None, 64, FP4_ROW_BYTES),
+                                          _arg(slots, "slots", torch.int32, n), n, _arg(kv, "kv", torch.bfloat16, n, 576),
+                                          kv_pool_fp4.shape[0], _ptr(status), _stream(stream)),
+               "mla_kv_dequantize_fp4")
+    return kv
+
+
+def fp4_pool_from(kv_pool, stream=None):
+    """The 4-bit copy of a whole bf16 pool [num_blocks][64][576] (every slot quantised)."""
+    nb = kv_pool.shape[0]
+    pool4 = torch.empty((nb, 64, FP4_ROW_BYTES), dtype=torch.uint8, device=kv_pool.device)
+    slots = torch.arange(nb * 64, dtype=torch.int32, device=kv_pool.device)
+    return kv_quantize_fp4(kv_pool.reshape(nb * 64, 576), slots, pool4, stream=stream)
+
+
+@dataclass
+class BatchTables:
+    """What :func:`build_tables` writes beside the block table (all int32, device)."""
+    seq_lens: torch.Tensor    # [B]        cached + new
+    cu_new: torch.Tensor      # [B + 1]    new tokens before each request
+    slots: torch.Tensor       # [max_new]  block * 64 + row of each new token, -1 behind the last
+    positions: torch.Tensor   # [max_new]  its position in its request, -1 behind the last
+    free_head: torch.Tensor   # [1]        the next free block
+
+    @classmethod
+    def empty(cls, B: int, max_new: int, device="cuda") -> "BatchTables":
+        buf = torch.empty(2 * B + 2 + 2 * max_new, dtype=torch.int32, device=device)
+        lens, cu, slots, pos, head = buf.split([B, B + 1, max_new, max_new, 1])
+        return cls(lens, cu, slots, pos, head)
+
+
+def build_tables(cached_lens, new_lens, block_table, free_blocks, free_head, max_new: int, num_blocks: int,
+                 out: BatchTables | None = None, status=None, stream=None) -> BatchTables:
+    """Block tables and slot maps of a step on the GPU, from the requests' lengths.
+
+    ``cached_lens``, ``new_lens`` int32 [B]; ``block_table`` int32 [B][max_blocks]
+    gains the new pages' blocks, taken from ``free_blocks[free_head[0]:]`` in
+    request order.  ``out.seq_lens`` may be ``cached_lens`` and
+    ``out.free_head`` may be ``free_head``: a captured step then moves on by itself.
+    """
+    B = cached_lens.shape[0]
+    if out is None:
+        out = BatchTables.empty(B, max_new, cached_lens.device)
+    i32 = torch.int32
+    with _on(cached_lens, new_lens, block_table, free_blocks, free_head, out.seq_lens, out.cu_new, out.slots,
+             out.positions, out.free_head, status):
+        _check(_lib.mla_build_tables(
+            B, _arg(cached_lens, "cached_lens", i32, B), _arg(new_lens, "new_lens", i32, B), block_table.shape[1],
+            _arg(block_table, "block_table", i32, B, None), _arg(free_blocks, "free_blocks", i32, None),
+            free_blocks.shape[0], _arg(free_head, "free_head", i32, 1), num_blocks, max_new,
+            _arg(out.seq_lens, "seq_lens", i32, B), _arg(out.cu_new, "cu_new", i32, B + 1),
+            _arg(out.slots, "slots", i32, max_new), _arg(out.positions, "positions", i32, max_new),
+            _arg(out.free_head, "free_head", i32, 1), _ptr(status), _stream(stream)), "mla_build_tables")
+    return out
+
+
+def plan_device(dims: MlaDims, seq_lens, num_clusters: int, plan_dev=None, status=None, stream=None):
+    """:func:`plan` made on the GPU from device ``seq_lens`` (int32 [B]; 0 is a
+    padded row without work): the same words, as an int32 device tensor."""
+    if plan_dev is None:
+        plan_dev = torch.empty(plan_size(dims, num_clusters)[0] // 4, dtype=torch.int32, device=seq_lens.device)
+    with _on(seq_lens, plan_dev, status):
+        _check(_lib.mla_plan_device(ctypes.byref(dims), _arg(seq_lens, "seq_lens", torch.int32, dims.B), num_clusters,
+                                    _arg(plan_dev, "plan_dev", torch.int32, None), plan_dev.nbytes, _ptr(status),
+                                    _stream(stream)), "mla_plan_device")
+    return plan_dev
+
+
+_POOL_ROWS = {"bf16": (torch.bfloat16, 576), "fp8": (torch.uint8, FP8_ROW_BYTES), "fp4": (torch.uint8, FP4_ROW_BYTES)}
+
+
+def summarize_pages(kv_pool, blocks, codes, scales, kv_cache: str = "bf16", status=None, stream=None):
+    """8-bit summaries (means) of full pages ``blocks`` (int32 [n]; -1 is
+    skipped) of a pool of kind ``kv_cache``, into ``codes`` int8 [num_blocks][576]
+    and ``scales`` fp32 [num_blocks]."""
+    if kv_cache not in CACHE_KINDS:
+        raise ValueError("kv_cache must be 'bf16', 'fp8' or 'fp4'")
+    nb, n = kv_pool.shape[0], blocks.shape[0]
+    dtype, row = _POOL_ROWS[kv_cache]
+    with _on(kv_pool, blocks, codes, scales, status):
+        _check(_lib.mla_summarize_pages(_arg(kv_pool, "kv_pool", dtype, nb, 64, row), CACHE_KINDS[kv_cache],
+                                        _arg(blocks, "blocks", torch.int32, n), n, nb,
+                                        _arg(codes, "codes", torch.int8, nb, 576),
+                                        _arg(scales, "scales", torch.float32, nb), _ptr(status), _stream(stream)),
+               "mla_summarize_pages")
+    return codes, scales
+
+
+def select_pages(dims: MlaDims, q_lat, q_rope, codes, scales, block_table, seq_lens, k: int, scores, sel_table,
+                 sel_lens, sel_pages=None, n_first: int = 1, n_recent: int = 1, status=None, stream=None):
+    """The pages each query row attends to: all of its pages if there are at most
+    ``k``, else the first ``n_first``, the last ``n_recent`` and the best scores.
+    Writes ``sel_table`` int32 [N][k] (a block table with one row per query),
+    ``sel_lens`` int32 [N] and, if given, ``sel_pages`` int32 [N][k]."""
+    N, H = dims.B * dims.s_q, dims.n_heads
+    i32 = torch.int32
+    with _on(q_lat, q_rope, codes, scales, block_table, seq_lens, scores, sel_table, sel_lens, sel_pages, status):
+        _check(_lib.mla_select_pages(
+            ctypes.byref(dims), _arg(q_lat, "q_lat", torch.bfloat16, N, H, 512),
+            _arg(q_rope, "q_rope", torch.bfloat16, N, H, 64), _arg(codes, "codes", torch.int8, dims.num_blocks, 576),
+            _arg(scales, "scales", torch.float32, dims.num_blocks),
+            _arg(block_table, "block_table", i32, dims.B, dims.max_blocks_per_seq),
+            _arg(seq_lens, "seq_lens", i32, dims.B), k, n_first, n_recent,
+            _arg(scores, "scores", torch.float32, N, dims.max_blocks_per_seq), _arg(sel_table, "sel_table", i32, N, k),
+            _arg(sel_lens, "sel_lens", i32, N), _arg(sel_pages, "sel_pages", i32, N, k), _ptr(status),
+            _stream(stream)), "mla_select_pages")
+    return sel_table, sel_lens, sel_pages
+
+
 def combine(dims, plan_dev, o_part, lse_part, o_lat, lse_out=None, stream=None):
     _check(_lib.mla_combine(ctypes.byref(dims), _ptr(plan_dev), _ptr(o_part), _ptr(lse_part),
                             _ptr(o_lat), _ptr(lse_out), _stream(stream)), "mla_combine")
@@ -380,10 +564,11 @@ class Decoder:
     def __init__(self, seq_lens, s_q: int, n_heads: int, max_blocks: int, num_blocks: int,
                  device="cuda", scale=None, causal=True, num_clusters: int | None = None,
                  kv_cache: str = "bf16"):
-        """``kv_cache``: "bf16" (pool [num_blocks][64][576] bf16) or "fp8" (pool
-        uint8 [num_blocks][64][656], see :func:`kv_quantize_fp8`)."""
-        if kv_cache not in ("bf16", "fp8"):
-            raise ValueError("kv_cache must be 'bf16' or 'fp8'")
+        """``kv_cache``: "bf16" (pool [num_blocks][64][576] bf16), "fp8" (pool
+        uint8 [num_blocks][64][656], see :func:`kv_quantize_fp8`) or "fp4" (pool
+        uint8 [num_blocks][64][416], see :func:`kv_quantize_fp4`)."""
+        if kv_cache not in CACHE_KINDS:
+            raise ValueError("kv_cache must be 'bf16', 'fp8' or 'fp4'")
         self.kv_cache = kv_cache
         self.seq_lens_host = np.asarray(seq_lens, dtype=np.int32)
         self.B = len(self.seq_lens_host)
@@ -421,12 +606,12 @@ class Decoder:
             absorb_q_fp8(q_nope, self.fp8_uk, self.q_lat, stream)
         else:
             absorb_q(q_nope, w_uk, self.q_lat, stream)
-        if draft_masks is not None and self.kv_cache == "fp8":
+        if draft_masks is not None and self.kv_cache != "bf16":
             raise ValueError("draft-tree masks need the bf16 cache")
-        if self.kv_cache == "fp8":
-            decode_attn_fp8cache(self.dims, self.q_lat, q_rope, kv_pool, block_table, self.seq_lens_dev,
-                                 self.plan_dev, self.num_clusters, self.o_part, self.lse_part, self.o_lat,
-                                 self.lse, self.status, stream)
+        if self.kv_cache != "bf16":
+            attn = decode_attn_fp8cache if self.kv_cache == "fp8" else decode_attn_fp4cache
+            attn(self.dims, self.q_lat, q_rope, kv_pool, block_table, self.seq_lens_dev, self.plan_dev,
+                 self.num_clusters, self.o_part, self.lse_part, self.o_lat, self.lse, self.status, stream)
         elif draft_masks is not None:
             decode_attn_tree(self.dims, self.q_lat, q_rope, kv_pool, block_table, self.seq_lens_dev, draft_masks,
                              self.plan_dev, self.num_clusters, self.o_part, self.lse_part, self.o_lat,
@@ -446,6 +631,65 @@ class Decoder:
     @property
     def launches_per_step(self) -> int:
         return 4 if self.num_slots > 0 else 3
+
+
+@dataclass
+class SparseOutputs:
+    o_lat: torch.Tensor      # bf16 [N][h][512]
+    lse: torch.Tensor        # fp32 [N][h], over the chosen pages
+    pages: torch.Tensor      # int32 [N][k] page numbers, -1 behind the last
+    table: torch.Tensor      # int32 [N][k] their blocks
+    lens: torch.Tensor       # int32 [N] keys attended
+    status: torch.Tensor     # int32 [1]
+
+
+class SparseAttention:
+    """Attention of each query over the pages a cheap score picks, for one batch
+    shape: :func:`select_pages`, :func:`plan_device` of the selection, the decode
+    kernel of the cache's kind and :func:`combine`.
+
+    Lengths stay on the device, so one captured ``run()`` serves a batch as it
+    grows, and rows of length 0 (a padded batch) are left as they were.  The
+    buffers are made here; one object's runs must not overlap.
+    """
+
+    def __init__(self, B: int, s_q: int, n_heads: int, max_blocks: int, num_blocks: int, k: int, n_first: int = 1,
+                 n_recent: int = 1, kv_cache: str = "bf16", device="cuda", scale=None, causal=True,
+                 num_clusters: int | None = None):
+        if kv_cache not in CACHE_KINDS:
+            raise ValueError("kv_cache must be 'bf16', 'fp8' or 'fp4'")
+        if n_first < 0 or n_recent < 1 or n_first + n_recent > k:
+            raise ValueError("n_first >= 0, n_recent >= 1 and n_first + n_recent <= k are needed")
+        self.kv_cache, self.k, self.n_first, self.n_recent = kv_cache, k, n_first, n_recent
+        self.num_clusters = num_clusters or max_clusters()
+        N = B * s_q
+        self.dims = make_dims(B, s_q, n_heads, max_blocks, num_blocks, scale, causal)
+        self.row_dims = make_dims(N, 1, n_heads, k, num_blocks, scale)   # a row is a sequence of its chosen pages
+        plan_bytes, o_bytes, lse_bytes = plan_size(self.row_dims, self.num_clusters)
+        dev = torch.device(device)
+        new = lambda *shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device=dev)
+        self.scores = new(N, max_blocks, dtype=torch.float32)
+        self.table, self.lens, self.pages = new(N, k), new(N), new(N, k)
+        self.plan_dev = new(plan_bytes // 4)
+        self.o_part, self.lse_part = new(o_bytes // 4, dtype=torch.float32), new(lse_bytes // 4, dtype=torch.float32)
+        self.o_lat = new(N, n_heads, 512, dtype=torch.bfloat16)
+        self.lse = new(N, n_heads, dtype=torch.float32)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def run(self, q_lat, q_rope, kv_pool, codes, scales, block_table, seq_lens, stream=None) -> SparseOutputs:
+        """``codes`` and ``scales``: the summaries of the pool's full pages
+        (:func:`summarize_pages`); ``seq_lens`` int32 [B] on the device."""
+        select_pages(self.dims, q_lat, q_rope, codes, scales, block_table, seq_lens, self.k, self.scores, self.table,
+                     self.lens, self.pages, self.n_first, self.n_recent, self.status, stream)
+        plan_device(self.row_dims, self.lens, self.num_clusters, self.plan_dev, self.status, stream)
+        dtype, row = _POOL_ROWS[self.kv_cache]
+        _arg(kv_pool, "kv_pool", dtype, self.dims.num_blocks, 64, row)
+        attn = {"bf16": decode_attn, "fp8": decode_attn_fp8cache, "fp4": decode_attn_fp4cache}[self.kv_cache]
+        with _on(kv_pool, q_lat):
+            attn(self.row_dims, q_lat, q_rope, kv_pool, self.table, self.lens, self.plan_dev, self.num_clusters,
+                 self.o_part, self.lse_part, self.o_lat, self.lse, self.status, stream)
+            combine(self.row_dims, self.plan_dev, self.o_part, self.lse_part, self.o_lat, self.lse, stream)
+        return SparseOutputs(self.o_lat, self.lse, self.pages, self.table, self.lens, self.status)
 
 
 class GraphedStep:

@@ -67,6 +67,16 @@ typedef enum {
                                         amax > 65504, beyond what mla_decode_attn_fp8cache widens
                                         (fp16); the row is written but must not be attended */
 
+#define MLA_STATUS_NO_SPACE    0x40  /* mla_build_tables: a request got no new tokens (no free block, longer
+                                        than its table row, no room in the slot map, or a bad length) */
+
+/* What a cache pool holds per token. */
+enum {
+  MLA_CACHE_BF16 = 0,  /* bf16 [576]                                             */
+  MLA_CACHE_FP8 = 1,   /* 656 bytes, see mla_decode_attn_fp8cache                */
+  MLA_CACHE_FP4 = 2    /* 416 bytes, see mla_decode_attn_fp4cache                */
+};
+
 /* Problem dimensions of one decode batch. */
 typedef struct {
   int32_t B;                  /* sequences */
@@ -277,6 +287,137 @@ mla_status_t mla_decode_attn_fp8cache(const mla_dims_t* dims, const void* q_lat,
  */
 mla_status_t mla_kv_quantize_fp8(const void* kv, const int32_t* slots, int64_t n, void* pool_fp8,
                                  int32_t num_blocks, int32_t* status, void* stream);
+
+/*
+ * mla_decode_attn_fp4cache -- mla_decode_attn on a 4-bit latent cache: 416
+ * bytes per token where bf16 takes 1152.  c_KV is kept in sixteen groups of 32
+ * columns with one fp16 scale each, in E2M1 codes (the values 0, .5, 1, 1.5, 2,
+ * 3, 4, 6 and their negatives are codes 0..7 and 8..15).  Token row:
+ *   bytes [0, 256)    codes, column 2i in the low nibble of byte i, 2i + 1 in the high one
+ *   bytes [256, 288)  fp16 scales s_0..s_15, c_KV[t, c] = code[c] * s_{c / 32}
+ *   bytes [288, 416)  k_rope[t, 0..63] in bf16 (not quantised)
+ *   kv_pool_fp4  uint8 [num_blocks][64][416], 16-byte aligned (mla_kv_quantize_fp4 writes it)
+ * Numerics: rows are widened on chip to fp16 (code * scale, rounded once), q_lat is rounded to
+ * fp16, P is written as fp16, and the products accumulate in fp32; the RoPE
+ * products are bf16, and partial scores are exchanged in fp16 as in
+ * mla_decode_attn.  |q_lat| <= 65504 (else MLA_STATUS_SCORE_RANGE).  All other
+ * arguments, outputs, status bits and the plan are those of mla_decode_attn;
+ * mla_combine completes split rows.  No draft-tree masks.
+ */
+mla_status_t mla_decode_attn_fp4cache(const mla_dims_t* dims, const void* q_lat, const void* q_rope,
+                                      const void* kv_pool_fp4, const int32_t* block_table,
+                                      const int32_t* seq_lens, const void* plan_dev, int32_t num_clusters,
+                                      float* o_part, float* lse_part, void* o_lat, float* lse_out,
+                                      int32_t* status, void* stream);
+
+/*
+ * mla_kv_quantize_fp4 -- write cache rows into 4-bit pool slots.  Per group of 32
+ * columns: s = fp16(max |x| / 6), code = E2M1(x / s) rounded to nearest even
+ * and saturated at 6 (s = 0: all codes 0); k_rope is copied.
+ *   kv        bf16 [n][576]  rows c_KV (512) | k_rope (64), 16-byte aligned
+ *   slots     int32 [n]      destination of row i: block * 64 + row in the block; -1: padding, the
+ *             row is skipped (the slot maps of mla_build_tables end in them)
+ *   pool_fp4  uint8 [num_blocks][64][416]
+ *   status    int32 [1] or NULL: MLA_STATUS_BAD_BLOCK when another slot lies outside the pool
+ *             (that row is not written); MLA_STATUS_CACHE_RANGE when a group holds a NaN or
+ *             max |x| > 65504 (written with the largest scale, 10912; must not be attended)
+ * Rows with equal slots race (each 16-byte piece is one of theirs).
+ *
+ * mla_kv_dequantize_fp4 -- read slots of a 4-bit pool back as bf16 rows (code * scale, rounded
+ * once): a cached prefix for the prefill path, which reads bf16 pools.
+ *   kv        bf16 [n][576], written; rows of padding (-1) and of bad slots are left as they were
+ */
+mla_status_t mla_kv_quantize_fp4(const void* kv, const int32_t* slots, int64_t n, void* pool_fp4,
+                                 int32_t num_blocks, int32_t* status, void* stream);
+mla_status_t mla_kv_dequantize_fp4(const void* pool_fp4, const int32_t* slots, int64_t n, void* kv,
+                                   int32_t num_blocks, int32_t* status, void* stream);
+
+/*
+ * mla_build_tables -- block tables and slot maps of a step on the GPU, from the
+ * requests' lengths: request b holds cached_lens[b] tokens in the cache and
+ * appends new_lens[b].  The new pages come from a list of free blocks, in
+ * request order; nothing is read back to the host, so a captured step replays
+ * as the requests grow.
+ *   cached_lens   int32 [B]   tokens already cached (>= 0)
+ *   new_lens      int32 [B]   tokens to append (>= 0; 0: none this step)
+ *   block_table   int32 [B][max_blocks_per_seq], in and out: the entries of cached pages are read
+ *                 (the last one, when new tokens go into it), those of new pages are written,
+ *                 all others stay
+ *   free_blocks   int32 [n_free], free_head int32 [1]: the next free block is free_blocks[free_head[0]]
+ *   num_blocks    blocks in the pool (entries outside are reported)
+ *   max_new       entries of slots and positions
+ *   seq_lens      int32 [B], written: cached_lens + new_lens (may be cached_lens itself)
+ *   cu_new        int32 [B + 1], written: new tokens before request b
+ *   slots         int32 [max_new], written: block * 64 + row of each new token, requests in order;
+ *                 -1 behind the last
+ *   positions     int32 [max_new] or NULL, written: the token's position in its request; -1 behind the last
+ *   free_head_out int32 [1], written: free_head + the blocks taken (may be free_head itself)
+ *   status        MLA_STATUS_NO_SPACE when a request gets nothing this step: its blocks do not fit the
+ *                 free list, cached + new does not fit its table row, its tokens do not fit max_new,
+ *                 or a length is negative.  Its seq_lens entry stays at cached_lens (0 if that is
+ *                 negative).  Requests are admitted in order: once one does not fit the free list no
+ *                 later one gets new blocks, once one does not fit max_new no later one gets tokens.
+ *                 MLA_STATUS_BAD_BLOCK when a block id read lies outside the pool (its slots are -1)
+ * 1 <= B <= 65536.  The arrays must not overlap except as said.
+ *
+ * mla_plan_device -- mla_plan on the GPU: the same plan, word for word, from
+ * device lengths, so that a captured decode step follows them.
+ *   seq_lens  int32 [B] (device).  0 is a padded row: it gets no work item, and
+ *             the attention and the merge leave its outputs as they were.  A
+ *             length below s_q or beyond max_blocks_per_seq * 64 is treated so
+ *             too, and reported (MLA_STATUS_BAD_SEQLEN)
+ *   plan_dev  device buffer of plan_bytes >= mla_plan_size's, written whole
+ * Give the attention o_part and lse_part of mla_plan_size's sizes, and always
+ * call mla_combine: the host does not see whether a row was split.
+ */
+mla_status_t mla_build_tables(int32_t B, const int32_t* cached_lens, const int32_t* new_lens,
+                              int32_t max_blocks_per_seq, int32_t* block_table, const int32_t* free_blocks,
+                              int32_t n_free, const int32_t* free_head, int32_t num_blocks, int32_t max_new,
+                              int32_t* seq_lens, int32_t* cu_new, int32_t* slots, int32_t* positions,
+                              int32_t* free_head_out, int32_t* status, void* stream);
+mla_status_t mla_plan_device(const mla_dims_t* dims, const int32_t* seq_lens, int32_t num_clusters, void* plan_dev,
+                             size_t plan_bytes, int32_t* status, void* stream);
+
+/*
+ * Sparse attention over pages.  Each query row attends to at most k pages of its
+ * sequence, chosen by a cheap score; the chosen pages go through any of the
+ * decode kernels as a block table of their own.
+ *
+ * mla_summarize_pages -- the 8-bit summary of full pages: the mean m of the
+ * page's 64 rows [c_KV | k_rope], scale = amax / 127, code = rint(127 m / amax)
+ * (0 and 0 when amax = 0).  Call it when a page fills; a page that still grows needs none (it
+ * is among the recent pages).
+ *   kv_pool   the pool, of kind `cache` (MLA_CACHE_BF16, _FP8 or _FP4)
+ *   blocks    int32 [n]  pages to summarise; -1 is skipped, others outside the pool are reported
+ *             (MLA_STATUS_BAD_BLOCK) and skipped
+ *   codes     int8 [num_blocks][576], 16-byte aligned, and scales fp32 [num_blocks]: the entries of
+ *             those blocks are written, the others stay
+ *
+ * mla_select_pages -- the pages of each query row n = b * s_q + i, whose keys are
+ * t < kv_len (T_b - s_q + 1 + i, or T_b when dims->causal = 0): all of them if
+ * there are at most k, else the first n_first, the last n_recent and the best
+ * scores of the rest, ties to the lowest page.  With the row's heads in the
+ * summaries' form (qcode_h, qscale_h over the 576 columns of [q_lat | q_rope]),
+ *   score = fp32( max_h((qcode_h . pcode) * qscale_h) * pscale ),
+ * exact up to that rounding.
+ *   block_table int32 [B][max_blocks_per_seq], seq_lens int32 [B] (0: padded row)
+ *   1 <= n_recent, n_first + n_recent <= k
+ *   scores    fp32 [N][max_blocks_per_seq] workspace
+ *   sel_table int32 [N][k], written: the chosen pages' blocks in page order, -1 behind the last
+ *   sel_lens  int32 [N], written: the tokens in them that the row sees (the last page is always
+ *             chosen, so only it can be partly filled)
+ *   sel_pages int32 [N][k] or NULL, written: the pages' numbers, -1 behind the last
+ *   status    MLA_STATUS_BAD_SEQLEN: a length below s_q or beyond the table (the row selects nothing);
+ *             MLA_STATUS_BAD_BLOCK: a scored page's block lies outside the pool (scored -inf)
+ * The attention then takes dims with B = N, s_q = 1 and max_blocks_per_seq = k,
+ * sel_table, sel_lens and a plan of sel_lens (mla_plan_device).  Queries must be finite.
+ */
+mla_status_t mla_summarize_pages(const void* kv_pool, int32_t cache, const int32_t* blocks, int32_t n,
+                                 int32_t num_blocks, void* codes, float* scales, int32_t* status, void* stream);
+mla_status_t mla_select_pages(const mla_dims_t* dims, const void* q_lat, const void* q_rope, const void* codes,
+                              const float* scales, const int32_t* block_table, const int32_t* seq_lens, int32_t k,
+                              int32_t n_first, int32_t n_recent, float* scores, int32_t* sel_table,
+                              int32_t* sel_lens, int32_t* sel_pages, int32_t* status, void* stream);
 
 /*
  * mla_combine -- log-sum-exp merge of the split pieces of each split row:
