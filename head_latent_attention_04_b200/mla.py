@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -116,36 +117,51 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+# The step's calls are launch-bound at decode sizes, so the checks of a call that
+# is right take a few attribute reads per tensor; the messages are made only for
+# one that is wrong.
 def _arg(t, name: str, dtype, *shape) -> int | None:
-    """Device address of a tensor argument of the given type and shape (a None
-    extent takes any), refused here when it is anything else."""
+    """Device address of a tensor argument of the given type and shape, refused
+    here when it is anything else (its device is checked by _on)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if len(shape) != t.dim() or any(w is not None and w != h for w, h in zip(shape, t.shape)):
-        want = ", ".join("*" if w is None else str(w) for w in shape)
-        raise ValueError(f"{name}: expected shape [{want}], got {list(t.shape)}")
-    return _ptr(t)
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name}: expected a contiguous tensor (the library assumes row-major layouts)")
+
+
+def _vec(t, name: str, dtype) -> int | None:
+    """_arg for an array of any shape."""
+    if t is None or (t.dtype is dtype and t.is_contiguous()):
+        return None if t is None else t.data_ptr()
+    return _arg(t, name, dtype, *t.shape)
 
 
 _SAME_DEVICE = contextlib.nullcontext()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _on(first, *others):
-    """The device of the tensors of one call, made current for the launch (a
-    launch goes to the current device, and its default stream is that device's)."""
-    dev = first.device
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors of one call on {dev} and {t.device}")
-    if not first.is_cuda:
-        raise ValueError(f"expected a CUDA tensor, got one on {dev}")
-    return _SAME_DEVICE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+def _on(*tensors):
+    """The device of the tensors of one call (None: an argument left out), made
+    current for the launch: a launch goes to the current device, and its default
+    stream is that device's."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors of one call on {tensors[0].device} and {t.device}")
+    if dev < 0:
+        raise ValueError(f"expected a CUDA tensor, got one on {tensors[0].device}")
+    return _SAME_DEVICE if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _stream(stream=None) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -326,32 +342,33 @@ def decode_attn_fp4cache(dims, q_lat, q_rope, kv_pool_fp4, block_table, seq_lens
             _arg(q_rope, "q_rope", torch.bfloat16, N, H, 64),
             _arg(kv_pool_fp4, "kv_pool_fp4", torch.uint8, dims.num_blocks, 64, FP4_ROW_BYTES),
             _arg(block_table, "block_table", torch.int32, dims.B, dims.max_blocks_per_seq),
-            _arg(seq_lens, "seq_lens", torch.int32, dims.B), _arg(plan_dev, "plan_dev", torch.int32, None),
-            num_clusters, _ptr(o_part), _ptr(lse_part), _arg(o_lat, "o_lat", torch.bfloat16, N, H, 512),
-            _arg(lse_out, "lse_out", torch.float32, N, H), _ptr(status), _stream(stream)), "mla_decode_attn_fp4cache")
+            _arg(seq_lens, "seq_lens", torch.int32, dims.B), _vec(plan_dev, "plan_dev", torch.int32),
+            num_clusters, _vec(o_part, "o_part", torch.float32),
+            _vec(lse_part, "lse_part", torch.float32), _arg(o_lat, "o_lat", torch.bfloat16, N, H, 512),
+            _arg(lse_out, "lse_out", torch.float32, N, H), _vec(status, "status", torch.int32), _stream(stream)), "mla_decode_attn_fp4cache")
 
 
 def kv_quantize_fp4(kv, slots, kv_pool_fp4, status=None, stream=None):
     """bf16 cache rows ``kv`` [n][576] -> slots ``slots`` (int32 [n], block * 64 +
     row; -1 is padding) of the 4-bit pool (uint8 [num_blocks][64][416])."""
-    n = slots.shape[0]
+    nb, n = kv_pool_fp4.shape[0], slots.shape[0]
     with _on(kv_pool_fp4, kv, slots, status):
         _check(_lib.mla_kv_quantize_fp4(_arg(kv, "kv", torch.bfloat16, n, 576), _arg(slots, "slots", torch.int32, n), n,
-                                        _arg(kv_pool_fp4, "kv_pool_fp4", torch.uint8, None, 64, FP4_ROW_BYTES),
-                                        kv_pool_fp4.shape[0], _ptr(status), _stream(stream)), "mla_kv_quantize_fp4")
+                                        _arg(kv_pool_fp4, "kv_pool_fp4", torch.uint8, nb, 64, FP4_ROW_BYTES),
+                                        nb, _vec(status, "status", torch.int32), _stream(stream)), "mla_kv_quantize_fp4")
     return kv_pool_fp4
 
 
 def kv_dequantize_fp4(kv_pool_fp4, slots, kv=None, status=None, stream=None):
     """Slots of a 4-bit pool -> bf16 rows ``kv`` [n][576] (rows of padding and of
     bad slots are left as they were; zeros when ``kv`` is made here)."""
-    n = slots.shape[0]
+    nb, n = kv_pool_fp4.shape[0], slots.shape[0]
     if kv is None:
         kv = torch.zeros((n, 576), dtype=torch.bfloat16, device=kv_pool_fp4.device)
     with _on(kv_pool_fp4, kv, slots, status):
-        _check(_lib.mla_kv_dequantize_fp4(_arg(kv_pool_fp4, "kv_pool_fp4", torch.uint8, None, 64, FP4_ROW_BYTES),
+        _check(_lib.mla_kv_dequantize_fp4(_arg(kv_pool_fp4, "kv_pool_fp4", torch.uint8, nb, 64, FP4_ROW_BYTES),
                                           _arg(slots, "slots", torch.int32, n), n, _arg(kv, "kv", torch.bfloat16, n, 576),
-                                          kv_pool_fp4.shape[0], _ptr(status), _stream(stream)),
+                                          nb, _vec(status, "status", torch.int32), _stream(stream)),
                "mla_kv_dequantize_fp4")
     return kv
 
@@ -397,22 +414,28 @@ def build_tables(cached_lens, new_lens, block_table, free_blocks, free_head, max
              out.positions, out.free_head, status):
         _check(_lib.mla_build_tables(
             B, _arg(cached_lens, "cached_lens", i32, B), _arg(new_lens, "new_lens", i32, B), block_table.shape[1],
-            _arg(block_table, "block_table", i32, B, None), _arg(free_blocks, "free_blocks", i32, None),
-            free_blocks.shape[0], _arg(free_head, "free_head", i32, 1), num_blocks, max_new,
+            _arg(block_table, "block_table", i32, B, block_table.shape[1]), _vec(free_blocks, "free_blocks", i32),
+            free_blocks.numel(), _arg(free_head, "free_head", i32, 1), num_blocks, max_new,
             _arg(out.seq_lens, "seq_lens", i32, B), _arg(out.cu_new, "cu_new", i32, B + 1),
             _arg(out.slots, "slots", i32, max_new), _arg(out.positions, "positions", i32, max_new),
-            _arg(out.free_head, "free_head", i32, 1), _ptr(status), _stream(stream)), "mla_build_tables")
+            _arg(out.free_head, "free_head", i32, 1), _vec(status, "status", torch.int32), _stream(stream)), "mla_build_tables")
     return out
+
+
+@functools.lru_cache(maxsize=256)
+def _plan_words(rows: int, num_clusters: int) -> int:
+    return plan_size(make_dims(rows, 1, 1, 1, 1), num_clusters)[0] // 4
 
 
 def plan_device(dims: MlaDims, seq_lens, num_clusters: int, plan_dev=None, status=None, stream=None):
     """:func:`plan` made on the GPU from device ``seq_lens`` (int32 [B]; 0 is a
     padded row without work): the same words, as an int32 device tensor."""
     if plan_dev is None:
-        plan_dev = torch.empty(plan_size(dims, num_clusters)[0] // 4, dtype=torch.int32, device=seq_lens.device)
+        words = _plan_words(dims.B * dims.s_q, num_clusters)
+        plan_dev = torch.empty(words, dtype=torch.int32, device=seq_lens.device)
     with _on(seq_lens, plan_dev, status):
         _check(_lib.mla_plan_device(ctypes.byref(dims), _arg(seq_lens, "seq_lens", torch.int32, dims.B), num_clusters,
-                                    _arg(plan_dev, "plan_dev", torch.int32, None), plan_dev.nbytes, _ptr(status),
+                                    _vec(plan_dev, "plan_dev", torch.int32), 4 * plan_dev.numel(), _vec(status, "status", torch.int32),
                                     _stream(stream)), "mla_plan_device")
     return plan_dev
 
@@ -432,7 +455,7 @@ def summarize_pages(kv_pool, blocks, codes, scales, kv_cache: str = "bf16", stat
         _check(_lib.mla_summarize_pages(_arg(kv_pool, "kv_pool", dtype, nb, 64, row), CACHE_KINDS[kv_cache],
                                         _arg(blocks, "blocks", torch.int32, n), n, nb,
                                         _arg(codes, "codes", torch.int8, nb, 576),
-                                        _arg(scales, "scales", torch.float32, nb), _ptr(status), _stream(stream)),
+                                        _arg(scales, "scales", torch.float32, nb), _vec(status, "status", torch.int32), _stream(stream)),
                "mla_summarize_pages")
     return codes, scales
 
@@ -453,7 +476,7 @@ def select_pages(dims: MlaDims, q_lat, q_rope, codes, scales, block_table, seq_l
             _arg(block_table, "block_table", i32, dims.B, dims.max_blocks_per_seq),
             _arg(seq_lens, "seq_lens", i32, dims.B), k, n_first, n_recent,
             _arg(scores, "scores", torch.float32, N, dims.max_blocks_per_seq), _arg(sel_table, "sel_table", i32, N, k),
-            _arg(sel_lens, "sel_lens", i32, N), _arg(sel_pages, "sel_pages", i32, N, k), _ptr(status),
+            _arg(sel_lens, "sel_lens", i32, N), _arg(sel_pages, "sel_pages", i32, N, k), _vec(status, "status", torch.int32),
             _stream(stream)), "mla_select_pages")
     return sel_table, sel_lens, sel_pages
 
