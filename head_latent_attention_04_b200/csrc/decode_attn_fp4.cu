@@ -96,7 +96,7 @@ __device__ __forceinline__ void report(int32_t* status, int bits) {
 }
 
 // Suspend-time hint of the pipeline waits (0: no hint, spin).
-constexpr uint32_t kWaitHintNs = 0;
+constexpr uint32_t kWaitHintNs = 200;
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile WaitCtl* wc) {
   return __all_sync(0xffffffffu, mbar_wait<false, kWaitHintNs>(bar, parity, wc));

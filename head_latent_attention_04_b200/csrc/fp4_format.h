@@ -36,7 +36,10 @@ __device__ __forceinline__ uint32_t cvt_f16x2_e2m1x2(uint32_t codes) {
 }
 
 // Eight E2M1 codes (low nibble first) times a group's scale pair s2 = (s, s)
-// -> four fp16 pairs: widened exactly, multiplied, rounded once.
+// -> four fp16 pairs: widened exactly, multiplied, rounded once.  The conversion
+// takes two codes at the rate of any other integer instruction (64 lanes a
+// clock per SM, measured; the E4M3 one runs at half of that), so a byte-permute table
+// look-up (19 instructions for 8 codes against these 8) was slower.
 __device__ __forceinline__ void dequant_e2m1x8_f16(uint32_t codes, uint32_t s2, uint32_t (&o)[4]) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t.reg .b32 x0, x1, x2, x3;\n\t"
       "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
