@@ -433,7 +433,8 @@ mla_status_t mla_summarize_pages(const void* kv_pool, int32_t cache, const int32
 mla_status_t mla_select_pages(const mla_dims_t* dims, const void* q_lat, const void* q_rope, const void* codes,
                               const float* scales, const int32_t* block_table, const int32_t* seq_lens, int32_t k,
                               int32_t n_first, int32_t n_recent, float* scores, int32_t* sel_table,
-                              int32_t* sel_lens, int32_t* sel_pages, int32_t* status, void* stream) {
+                              int32_t* sel_lens, int32_t* sel_pages, int32_t num_clusters, void* plan_dev,
+                              size_t plan_bytes, int32_t* status, void* stream) {
   clear_error();
   MLA_TRY(check_dims(dims));
   if ((int64_t)dims->max_blocks_per_seq * 64 > INT32_MAX - 64)
@@ -451,9 +452,17 @@ mla_status_t mla_select_pages(const mla_dims_t* dims, const void* q_lat, const v
   MLA_TRY(check_words(sel_table, "sel_table"));
   MLA_TRY(check_words(sel_lens, "sel_lens"));
   MLA_TRY(check_optional_words(sel_pages, "sel_pages"));
+  MLA_TRY(check_optional_words(plan_dev, "plan_dev"));
   MLA_TRY(check_optional_words(status, "status"));
+  if (plan_dev) {
+    if (num_clusters < 1 || num_clusters > 4096)
+      return set_error(MLA_ERR_INVALID_ARG, "num_clusters must be in [1, 4096]");
+    if (plan_bytes < (size_t)plan_words_upper_bound(num_clusters, dims->B * dims->s_q) * 4)
+      return set_error(MLA_ERR_WORKSPACE_TOO_SMALL, "plan buffer smaller than mla_plan_size");
+  }
   return launch_select_pages(*dims, q_lat, q_rope, codes, scales, block_table, seq_lens, k, n_first, n_recent, scores,
-                             sel_table, sel_lens, sel_pages, status, stream);
+                             sel_table, sel_lens, sel_pages, num_clusters, static_cast<int32_t*>(plan_dev), status,
+                             stream);
 }
 
 mla_status_t mla_combine(const mla_dims_t* dims, const void* plan_dev, const float* o_part,

@@ -87,7 +87,7 @@ mla_status_t launch_summarize_pages(const void* kv_pool, int kind, const int32_t
 mla_status_t launch_select_pages(const mla_dims_t& d, const void* q_lat, const void* q_rope, const void* codes,
                                  const float* scales, const int32_t* block_table, const int32_t* seq_lens, int k,
                                  int n_first, int n_recent, float* scores, int32_t* sel_table, int32_t* sel_lens,
-                                 int32_t* sel_pages, int32_t* status, void* stream);
+                                 int32_t* sel_pages, int num_clusters, int32_t* plan, int32_t* status, void* stream);
 mla_status_t launch_combine(const mla_dims_t& d, const int32_t* plan_dev, int32_t n_rows,
                             const float* o_part, const float* lse_part, void* o_lat,
                             float* lse_out, void* stream);

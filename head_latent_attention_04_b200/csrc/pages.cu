@@ -18,6 +18,7 @@
 #include "block_scan.cuh"
 #include "fp4_format.h"
 #include "mla_internal.h"
+#include "plan_device.cuh"
 #include "ptx.cuh"
 
 #include <cuda_bf16.h>
@@ -150,10 +151,12 @@ summarize_pages_kernel(const uint8_t* __restrict__ pool, const int32_t* __restri
 // integers: D[page][head] = pcode . qcode, M = 128 pages, N = 128 heads, K = 576
 // in 18 steps of 32.  The row's heads are quantised once into shared memory (B,
 // K-major); a tile's summaries are gathered through the block table by
-// 16-byte asynchronous copies (A, K-major).  Bound by latency at the sizes of
-// a decode step (4 rows x 2048 pages are 4.8 MB and 1.2 GFLOP), so the grid
-// cuts a row into as many runs as fill the card and the blocks of many rows
-// walk a whole row, reusing its quantised heads.
+// 16-byte asynchronous copies (A, K-major; two buffers, and two in tensor
+// memory), so that a tile's product and the next tile's copies run under the
+// maxima of the tile before.  At one tile a block (4 rows of 2048 pages on 148
+// SMs) it is all latency: 6.9 us, of which 2.2 are two dependent reads and the
+// quantisation of 147 KB of queries; where a block walks its row a tile costs
+// 0.9 us.  The grid cuts a row into as many runs as fill the card.
 constexpr int kScoreThreads = 512;
 constexpr int kTile = 128;
 constexpr int kChunkBytes = kTile * 128;          // 128 rows x 128 K-bytes (SW128)
@@ -164,12 +167,12 @@ constexpr int kMaxHeads = 128;
 struct ScoreShared {
   float qscale[kMaxHeads];
   float2 best[4][kTile];
-  int block[kTile];
-  uint64_t done;
+  float scale[kTile];      // of the current tile's summaries, negative for a bad block
+  uint64_t done[2];
   uint32_t tmem;
   int ok;
 };
-constexpr int kScoreSmem = 2 * kOperandBytes + (int)sizeof(ScoreShared) + 1024;
+constexpr int kScoreSmem = 3 * kOperandBytes + (int)sizeof(ScoreShared) + 1024;
 
 struct SelectParams {
   const __nv_bfloat16* q_lat;
@@ -183,7 +186,9 @@ struct SelectParams {
   int32_t* sel_lens;
   int32_t* sel_pages;
   int32_t* status;
-  int s_q, causal, n_heads, max_blocks, num_blocks, k, n_first, n_recent;
+  int32_t* plan;   // plan of the selection, or null
+  PlanShape shape;
+  int N, s_q, causal, n_heads, max_blocks, num_blocks, k, n_first, n_recent;
 };
 
 // Keys that query row n attends (0 for a padded or inconsistent row).
@@ -223,30 +228,43 @@ constexpr uint32_t kIdescI8 = (2u << 4)            // D format s32
                               | (1u << 10)         // B format s8
                               | ((kMaxHeads >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
 
-// rint(127 x / amax) with r = 127 / amax: the product is within 2^-23 of the
-// quotient (relative); a quotient half-way between two integers has at most
-// 8 significant bits and any other is at least 2^-16 away from it (x and amax
-// have 8 significant bits), so rounding to 19 bits first puts the exact ties
-// back onto the tie and moves nothing across one.
-__device__ __forceinline__ int code_of(float x, float r) {
-  const float y = __uint_as_float((__float_as_uint(x * r) + 0x10u) & ~0x1Fu);
-  return __float2int_rn(y);
+// rint(127 x / amax) in one multiply-add per element: x r + 1.5 x 2^23, with the
+// product unrounded, leaves the rounded integer (ties to even) in the low bits.
+// For the exact quotients' codes r = 127 / amax must not move a half-way case.  x and amax
+// have 8 significant bits, so a quotient 127 x / amax that is not half-way between
+// two integers is at least 2^-16 (relative) away from it, far more than r's error.
+// Half-way cases: 254 x = (2k + 1) amax.  127 is prime, so it divides amax's significand (254:
+// r is then exact) or 2k + 1 = 127, which is x = amax / 2, half-way between 63
+// and 64 and due at 64: an inexact r is taken above 127 / amax, which sends it there.
+constexpr float kRound = 12582912.f;
+__device__ __forceinline__ float code_factor(float amax) {
+  const float r = 127.f / amax;
+  return __fmaf_rn(r, amax, -127.f) == 0.f ? r : r * (1.f + 0x1p-22f);
+}
+// Codes of the four bf16 values of two words; `up` is a power of two that both x and r's amax carry.
+__device__ __forceinline__ uint32_t code_word(uint32_t w0, uint32_t w1, float r, float up) {
+  const float x[4] = {__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xFFFF0000u), __uint_as_float(w1 << 16),
+                      __uint_as_float(w1 & 0xFFFF0000u)};
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = __float_as_uint(__fmaf_rn(x[i] * up, r, kRound));
+  return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
 }
 
 __global__ void __launch_bounds__(kScoreThreads, 1)
 score_pages_kernel(const SelectParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* s_a = smem;
-  uint8_t* s_b = smem + kOperandBytes;
-  ScoreShared* sh = reinterpret_cast<ScoreShared*>(smem + 2 * kOperandBytes);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (threadIdx.x == 0) {
-    mbar_init(&sh->done, 1);
+  uint8_t* s_b = smem + 2 * kOperandBytes;
+  ScoreShared* sh = reinterpret_cast<ScoreShared*>(smem + 3 * kOperandBytes);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  if (tid == 0) {
+    mbar_init(&sh->done[0], 1);
+    mbar_init(&sh->done[1], 1);
     fence_mbar_init();
   }
   if (warp == 0) {
-    tmem_alloc(&sh->tmem, 128);
+    tmem_alloc(&sh->tmem, 256);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -257,157 +275,203 @@ score_pages_kernel(const SelectParams p) {
   griddep_launch_dependents();
 
   const int n = blockIdx.x;
+  const int32_t* row = p.table + (size_t)(n / p.s_q) * p.max_blocks;
+  const uint32_t a_addr = smem_u32(smem), b_addr = smem_u32(s_b);
+  // A warp gathers eight rows of a tile.  Its block ids (lanes 0 .. 7) are read before
+  // it is known whether the row is that long (the table has max_blocks columns
+  // whatever its length).
+  auto read_id = [&](int t) {
+    const long long pg = (long long)t * kTile + 8 * warp + lane;
+    return lane < 8 && pg < p.max_blocks ? row[pg] : -1;
+  };
+  const int step = gridDim.y;
+  int tile = blockIdx.y;
+  int id_next = read_id(tile);
   bool bad = false;
   const int kv = select_keys(p, n, &bad);
   const int pages = (kv + kPage - 1) / kPage;
   const int scored = pages > p.k ? pages - p.n_recent : 0;   // pages [n_first, scored) compete
   const int tiles = (scored + kTile - 1) / kTile;
-  const int32_t* row = p.table + (size_t)(n / p.s_q) * p.max_blocks;
-  const uint32_t a_addr = smem_u32(s_a), b_addr = smem_u32(s_b);
 
-  // A: gathers tile t (asynchronous; rows past the last page and rows of bad
-  // blocks keep whatever they held, their scores are not used)
-  auto load_tile = [&](int t) {
-    if (threadIdx.x < kTile) {
-      const int pg = t * kTile + threadIdx.x;
-      int blk = pg < scored ? row[pg] : -1;
-      if (pg < scored && (blk < 0 || blk >= p.num_blocks)) {
+  // Takes the ids of tile t (read earlier) and starts its gather into A buffer b;
+  // returns the summary scale of lane l's row (l < 8), -1 for a bad block.  Rows behind the
+  // last page and rows of bad blocks keep whatever they held, their scores are not used.
+  auto gather = [&](int t, int b, int id) {
+    float scale = -1.f;
+    if (lane < 8) {
+      if (t * kTile + 8 * warp + lane >= scored) id = -1;
+      else if (id < 0 || id >= p.num_blocks) {
         report(p.status, MLA_STATUS_BAD_BLOCK);
-        blk = -1;
+        id = -1;
       }
-      sh->block[threadIdx.x] = blk;
+      if (id >= 0) scale = __ldg(p.scales + id);
     }
-    __syncthreads();
+    // chunks 0 .. 31 of row j go through lanes 0 .. 31, the last four of all eight rows together
+    const uint32_t a = a_addr + b * kOperandBytes;
 #pragma unroll
-    for (int i = threadIdx.x; i < kTile * 36; i += kScoreThreads) {
-      const int r = i / 36, c = i - 36 * r;
-      const int blk = sh->block[r];
-      if (blk >= 0) cp_async16(a_addr + operand_off(r, c), p.codes + (size_t)blk * kDim + 16 * c);
+    for (int j = 0; j < 8; ++j) {
+      const int blk = __shfl_sync(0xffffffffu, id, j);
+      if (blk >= 0) cp_async16(a + operand_off(8 * warp + j, lane), p.codes + (size_t)blk * kDim + 16 * lane);
     }
+    const int blk = __shfl_sync(0xffffffffu, id, lane >> 2);
+    if (blk >= 0)
+      cp_async16(a + operand_off(8 * warp + (lane >> 2), 32 + (lane & 3)),
+                 p.codes + (size_t)blk * kDim + 512 + 16 * (lane & 3));
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    return scale;
   };
-
-  if ((int)blockIdx.y < tiles) {
-    load_tile(blockIdx.y);
-    // B: a warp quantises eight heads; lane l takes the 8-column chunks l, l + 32 and (l < 8) l + 64
-#pragma unroll 1
-    for (int hh = 0; hh < kMaxHeads / 16; hh += 4) {
-      uint4 v[4][3];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int h = warp * 8 + hh + j;
-        const size_t at = (size_t)n * p.n_heads + h;
-        const bool in = h < p.n_heads;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        v[j][0] = in ? __ldg(reinterpret_cast<const uint4*>(p.q_lat + at * 512) + lane) : zero;
-        v[j][1] = in ? __ldg(reinterpret_cast<const uint4*>(p.q_lat + at * 512) + 32 + lane) : zero;
-        v[j][2] = in && lane < 8 ? __ldg(reinterpret_cast<const uint4*>(p.q_rope + at * 64) + lane) : zero;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int h = warp * 8 + hh + j;
-        float x[24];
-#pragma unroll
-        for (int e = 0; e < 3; ++e) {
-          const uint32_t w[4] = {v[j][e].x, v[j][e].y, v[j][e].z, v[j][e].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[8 * e + 2 * i] = __uint_as_float(w[i] << 16);
-            x[8 * e + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-          }
-        }
-        float amax = 0.f;
-#pragma unroll
-        for (int i = 0; i < 24; ++i) amax = fmaxf(amax, fabsf(x[i]));
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-        if (lane == 0) sh->qscale[h] = amax / 127.f;
-        const float up = amax < 0x1p-60f ? 0x1p80f : 1.f;   // keeps 127 / amax finite
-        const float r = amax > 0.f ? 127.f / (amax * up) : 0.f;
-#pragma unroll
-        for (int e = 0; e < 3; ++e) {
-          if (e == 2 && lane >= 8) break;
-          uint32_t o[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float* xe = x + 8 * e + 4 * i;
-            o[i] = (uint32_t)(code_of(xe[0] * up, r) & 255) | (uint32_t)(code_of(xe[1] * up, r) & 255) << 8 |
-                   (uint32_t)(code_of(xe[2] * up, r) & 255) << 16 | (uint32_t)(code_of(xe[3] * up, r) & 255) << 24;
-          }
-          const int chunk8 = lane + 32 * e;   // 8 bytes of codes: half of a 16-byte chunk
-          *reinterpret_cast<uint2*>(s_b + operand_off(h, chunk8 >> 1) + 8 * (chunk8 & 1)) = make_uint2(o[0], o[1]);
-        }
-      }
-    }
-  }
-  int it = 0;
-  bool ok = true;
-  for (int t = blockIdx.y; t < tiles; t += gridDim.y, ++it) {
-    cp_async_wait_all();
+  auto multiply = [&](int b, bool one_more_in_flight) {
+    if (one_more_in_flight) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
     fence_proxy_async_smem();
+    tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
       tc_fence_after();
-      const uint64_t ad = sdesc(a_addr, 16, 1024, kSwizzle128B), bd = sdesc(b_addr, 16, 1024, kSwizzle128B);
+      const uint32_t a = a_addr + b * kOperandBytes, d = tmem + 128 * b;
+      const uint64_t ad = sdesc(a, 16, 1024, kSwizzle128B), bd = sdesc(b_addr, 16, 1024, kSwizzle128B);
 #pragma unroll
       for (int s = 0; s < 16; ++s) {
         const uint64_t off = (uint64_t)(((s >> 2) * kChunkBytes + (s & 3) * 32) >> 4);
-        mma_ss_i8(tmem, ad + off, bd + off, kIdescI8, s != 0);
+        mma_ss_i8(d, ad + off, bd + off, kIdescI8, s != 0);
       }
-      const uint64_t at = sdesc(a_addr + 4 * kChunkBytes, 16, 512, kSwizzle64B);
+      const uint64_t at = sdesc(a + 4 * kChunkBytes, 16, 512, kSwizzle64B);
       const uint64_t bt = sdesc(b_addr + 4 * kChunkBytes, 16, 512, kSwizzle64B);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) mma_ss_i8(tmem, at + 2 * s, bt + 2 * s, kIdescI8, 1);
-      mma_commit(&sh->done);
-      sh->ok = mbar_drain(&sh->done, it & 1);
+      for (int s = 0; s < 2; ++s) mma_ss_i8(d, at + 2 * s, bt + 2 * s, kIdescI8, 1);
+      mma_commit(&sh->done[b]);
     }
-    const int blk = threadIdx.x < kTile ? sh->block[threadIdx.x] : -1;
+  };
+
+  float scale[2] = {-1.f, -1.f};
+  if (tile < tiles) {
+    // B: a warp quantises eight heads; lane l takes the 8-column chunks l, l + 32
+    // and (l < 8) l + 64 of each
+    uint4 v[8][3];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const size_t at = (size_t)n * p.n_heads + 8 * warp + j;
+      const bool in = 8 * warp + j < p.n_heads;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      v[j][0] = in ? __ldg(reinterpret_cast<const uint4*>(p.q_lat + at * 512) + lane) : zero;
+      v[j][1] = in ? __ldg(reinterpret_cast<const uint4*>(p.q_lat + at * 512) + 32 + lane) : zero;
+      v[j][2] = in && lane < 8 ? __ldg(reinterpret_cast<const uint4*>(p.q_rope + at * 64) + lane) : zero;
+    }
+    scale[0] = gather(tile, 0, id_next);
+    id_next = tile + step < tiles ? read_id(tile + step) : -1;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int h = 8 * warp + j;
+      uint32_t m = 0;   // largest magnitudes, a pair of bf16 (their signs come out meaningless)
+#pragma unroll
+      for (int e = 0; e < 3; ++e) {
+        const uint32_t w[4] = {v[j][e].x, v[j][e].y, v[j][e].z, v[j][e].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("max.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+      }
+      m = max(m & 0x7FFFu, (m >> 16) & 0x7FFFu);       // (as integers they order like the values)
+      m = __reduce_max_sync(0xffffffffu, m);
+      float amax = __uint_as_float(m << 16);
+      if (lane == 0) sh->qscale[h] = amax / 127.f;
+      const float up = amax < 0x1p-60f ? 0x1p80f : 1.f;   // keeps 127 / amax finite
+      const float r = m > 0 ? code_factor(amax * up) : 0.f;
+#pragma unroll
+      for (int e = 0; e < 3; ++e) {
+        if (e == 2 && lane >= 8) break;
+        const int chunk8 = lane + 32 * e;   // 8 bytes of codes: half of a 16-byte chunk
+        *reinterpret_cast<uint2*>(s_b + operand_off(h, chunk8 >> 1) + 8 * (chunk8 & 1)) =
+            make_uint2(code_word(v[j][e].x, v[j][e].y, r, up), code_word(v[j][e].z, v[j][e].w, r, up));
+      }
+    }
+    const bool more = tile + step < tiles;
+    if (more) {
+      scale[1] = gather(tile + step, 1, id_next);
+      id_next = tile + 2 * step < tiles ? read_id(tile + 2 * step) : -1;
+    }
+    multiply(0, more);
+  }
+  bool ok = true;
+#pragma unroll 1
+  for (int it = 0; tile < tiles; tile += step, ++it) {
+    const int b = it & 1;
+    if (tid == 0) sh->ok = mbar_drain(&sh->done[b], (it >> 1) & 1);
     __syncthreads();
     ok = sh->ok != 0;   // block-uniform
     if (!ok) break;
     tc_fence_after();
-    if (t + (int)gridDim.y < tiles) load_tile(t + gridDim.y);
-    // thread = (page, 32 heads): the largest dot x qscale as an exact pair hi + lo
+    if (lane < 8) sh->scale[8 * warp + lane] = b ? scale[1] : scale[0];
+    if (tile + step < tiles) multiply(b ^ 1, false);   // the next tile's copies are the only ones in flight
+    if (tile + 2 * step < tiles) {
+      const float s = gather(tile + 2 * step, b, id_next);
+      if (b) scale[1] = s; else scale[0] = s;
+      id_next = tile + 3 * step < tiles ? read_id(tile + 3 * step) : -1;
+    }
+    // thread = (page, 32 heads): the largest dot x qscale as an exact pair.  hi is the
+    // largest rounded product; the largest product itself rounds to it, so it is
+    // hi plus the largest of fma(dot, qscale, -hi), exact for the products that round to hi.
     const int quarter = warp & 3, group = warp >> 2;
-    uint32_t d[32];
-    tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + 32 * group, d);
-    tmem_ld_wait();
-    tc_fence_before();
-    float hi = -CUDART_INF_F, lo = 0.f;
+    const int heads = min(p.n_heads - 32 * group, 32);
+    float hi = -CUDART_INF_F, lo = -CUDART_INF_F;
+    if (heads > 0) {
+      uint32_t d[32];
+      tmem_ld32(tmem + 128 * b + ((uint32_t)(quarter * 32) << 16) + 32 * group, d);
+      tmem_ld_wait();
+      tc_fence_before();
+      const float4* qs = reinterpret_cast<const float4*>(sh->qscale + 32 * group);
+      if (heads == 32) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float f = (float)(int)d[i], s = sh->qscale[32 * group + i];
-      const float h = f * s, l = __fmaf_rn(f, s, -h);
-      const bool better = (h > hi || (h == hi && l > lo)) && 32 * group + i < p.n_heads;
-      hi = better ? h : hi;
-      lo = better ? l : lo;
+        for (int i = 0; i < 32; i += 4) {
+          const float4 s = qs[i / 4];
+          hi = fmaxf(fmaxf(hi, fmaxf((float)(int)d[i] * s.x, (float)(int)d[i + 1] * s.y)),
+                     fmaxf((float)(int)d[i + 2] * s.z, (float)(int)d[i + 3] * s.w));
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const float4 s = qs[i / 4];
+          lo = fmaxf(fmaxf(lo, fmaxf(__fmaf_rn((float)(int)d[i], s.x, -hi), __fmaf_rn((float)(int)d[i + 1], s.y, -hi))),
+                     fmaxf(__fmaf_rn((float)(int)d[i + 2], s.z, -hi), __fmaf_rn((float)(int)d[i + 3], s.w, -hi)));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i < heads) hi = fmaxf(hi, (float)(int)d[i] * sh->qscale[32 * group + i]);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i < heads) lo = fmaxf(lo, __fmaf_rn((float)(int)d[i], sh->qscale[32 * group + i], -hi));
+      }
     }
     sh->best[group][quarter * 32 + lane] = make_float2(hi, lo);
     __syncthreads();
-    if (threadIdx.x < kTile) {
-      float2 b = sh->best[0][threadIdx.x];
+    if (tid < kTile) {
+      float2 best = sh->best[0][tid];
 #pragma unroll
       for (int g = 1; g < 4; ++g) {
-        const float2 o = sh->best[g][threadIdx.x];
-        if (o.x > b.x || (o.x == b.x && o.y > b.y)) b = o;
+        const float2 o = sh->best[g][tid];
+        if (o.x > best.x || (o.x == best.x && o.y > best.y)) best = o;
       }
-      const int pg = t * kTile + threadIdx.x;
+      const int pg = tile * kTile + tid;
+      const float scale_of = sh->scale[tid];
       if (pg < scored)
         p.scores[(size_t)n * p.max_blocks + pg] =
-            blk >= 0 ? (float)(((double)b.x + (double)b.y) * (double)p.scales[blk]) : -CUDART_INF_F;
+            scale_of >= 0.f ? (float)(((double)best.x + (double)best.y) * (double)scale_of) : -CUDART_INF_F;
     }
   }
-  if (!ok && threadIdx.x == 0) report(p.status, MLA_STATUS_TIMEOUT);
-  cp_async_wait_all();
+  if (!ok) {
+    if (tid == 0) report(p.status, MLA_STATUS_TIMEOUT);
+    cp_async_wait_all();
+  }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) tmem_dealloc(tmem, 128);
+  if (warp == 0) tmem_dealloc(tmem, 256);
 }
 
 // ---------------------------------------------------------------- selection
 // One block per query row: the k-th best score by a radix search on its
 // ordered bits (11, 11 and 10 of them, histograms in shared memory), then one
 // ordered pass that writes the pages above it, and the first of those equal to
-// it, in page order.  Latency: three histogram passes over the row's scores.
+// it, in page order.  Latency: three histogram passes over the row's scores.  How
+// many pages and keys a row gets follows from its length alone, so one more block
+// makes the attention's split-KV plan meanwhile.
 constexpr int kSelThreads = 1024;
 constexpr int kBins = 2048;
 
@@ -418,13 +482,26 @@ __device__ __forceinline__ uint32_t order_key(float score) {
 
 __global__ void __launch_bounds__(kSelThreads)
 select_pages_kernel(const SelectParams p) {
-  __shared__ int s_hist[kBins];
+  __shared__ union {
+    int hist[3][kBins];
+    PlanScratch plan;
+  } sh;
   __shared__ int s_warp[32];
   __shared__ int s_digit, s_above;
+  for (int i = threadIdx.x; i < 3 * kBins; i += kSelThreads) sh.hist[0][i] = 0;
   griddep_wait();
   griddep_launch_dependents();
   const int n = blockIdx.x, t = threadIdx.x;
   bool bad = false;
+  if (n == p.N) {   // the last block: the plan of the selection, whose lengths need no scores
+    __syncthreads();   // (the zeroes above lie where the plan's scratch does)
+    make_plan(p.shape, sh.plan, p.plan, [&](int i) {
+      const int kv = select_keys(p, i, &bad);
+      const int pages = (kv + kPage - 1) / kPage;
+      return kv - (pages - min(pages, p.k)) * kPage;
+    });
+    return;
+  }
   const int kv = select_keys(p, n, &bad);
   if (bad && t == 0) report(p.status, MLA_STATUS_BAD_SEQLEN);
   const int pages = (kv + kPage - 1) / kPage;
@@ -447,24 +524,38 @@ select_pages_kernel(const SelectParams p) {
   if (want == 0) return;
   const int begin = p.n_first, end = pages - p.n_recent;   // end - begin > want
   const float* scores = p.scores + (size_t)n * p.max_blocks;
+  // up to 4096 candidates stay in registers from here on; more are read again in each pass
+  constexpr int kHeld = 4;
+  const bool held = end - begin <= kHeld * kSelThreads;
+  uint32_t key[kHeld];
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) {
+    const int i = begin + h * kSelThreads + t;
+    key[h] = held && i < end ? order_key(scores[i]) : 0;
+  }
+  __syncthreads();   // the histograms are zero
 
   // key bits found so far; after the last digit the threshold itself
   uint32_t prefix = 0;
-  const int shifts[3] = {21, 10, 0}, widths[3] = {11, 11, 10};
-#pragma unroll 1
+#pragma unroll
   for (int d = 0; d < 3; ++d) {
-    const int shift = shifts[d], bins = 1 << widths[d];
-    for (int i = t; i < bins; i += kSelThreads) s_hist[i] = 0;
-    __syncthreads();
-    for (int i = begin + t; i < end; i += kSelThreads) {
-      const uint32_t key = order_key(scores[i]);
-      if (d == 0 || (key >> (shift + widths[d])) == prefix) atomicAdd(&s_hist[(key >> shift) & (bins - 1)], 1);
+    const int width = d == 2 ? 10 : 11, shift = d == 0 ? 21 : d == 1 ? 10 : 0, bins = 1 << width;
+    int* hist = sh.hist[d];
+    auto count = [&](uint32_t k) {
+      if (d == 0 || (k >> ((shift + width) & 31)) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
+    };
+    if (held) {
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h)
+        if (begin + h * kSelThreads + t < end) count(key[h]);
+    } else {
+      for (int i = begin + t; i < end; i += kSelThreads) count(order_key(scores[i]));
     }
     __syncthreads();
-    // thread t holds the bins (from the top) 2t and 2t + 1
-    const int per = bins / kSelThreads;   // 2 or 1
+    // thread t holds the bins (from the top) 2t and 2t + 1, or t of the last digit's 1024
+    const int per = bins / kSelThreads;
     const int top = bins - 1 - per * t;
-    const int c0 = s_hist[top], c1 = per == 2 ? s_hist[top - 1] : 0;
+    const int c0 = hist[top], c1 = per == 2 ? hist[top - 1] : 0;
     int all;
     const int incl = block_scan<int>(c0 + c1, s_warp, &all);
     const int before = incl - c0 - c1;
@@ -474,16 +565,14 @@ select_pages_kernel(const SelectParams p) {
       s_above = second ? before + c0 : before;
     }
     __syncthreads();
-    prefix = (prefix << widths[d]) | (uint32_t)s_digit;
+    prefix = (prefix << width) | (uint32_t)s_digit;
     want -= s_above;      // still to take among the keys with this prefix
     __syncthreads();
   }
   // `want` of the pages equal to the threshold, in page order
   int above_before = 0, equal_before = 0;
-  for (int i0 = begin; i0 < end; i0 += kSelThreads) {
-    const int i = i0 + t;
-    const uint32_t key = i < end ? order_key(scores[i]) : 0;
-    const bool above = i < end && key > prefix, equal = i < end && key == prefix;
+  auto take = [&](int i, uint32_t k) {
+    const bool above = i < end && k > prefix, equal = i < end && k == prefix;
     int all;
     const int incl = block_scan<int>((above ? 1 : 0) | (equal ? 1 << 16 : 0), s_warp, &all);
     const int a = above_before + (incl & 0xFFFF) - (above ? 1 : 0);
@@ -491,6 +580,16 @@ select_pages_kernel(const SelectParams p) {
     if (above || (equal && e < want)) put(p.n_first + a + min(e, want), i);
     above_before += all & 0xFFFF;
     equal_before += all >> 16;
+  };
+  if (held) {
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h)
+      if (begin + h * kSelThreads < end) take(begin + h * kSelThreads + t, key[h]);
+  } else {
+    for (int i0 = begin; i0 < end; i0 += kSelThreads) {
+      const int i = i0 + t;
+      take(i, i < end ? order_key(scores[i]) : 0);
+    }
   }
 }
 
@@ -524,12 +623,14 @@ mla_status_t launch_summarize_pages(const void* kv_pool, int kind, const int32_t
 mla_status_t launch_select_pages(const mla_dims_t& d, const void* q_lat, const void* q_rope, const void* codes,
                                  const float* scales, const int32_t* block_table, const int32_t* seq_lens, int k,
                                  int n_first, int n_recent, float* scores, int32_t* sel_table, int32_t* sel_lens,
-                                 int32_t* sel_pages, int32_t* status, void* stream) {
+                                 int32_t* sel_pages, int num_clusters, int32_t* plan, int32_t* status, void* stream) {
+  const int N = d.B * d.s_q;
+  const PlanShape shape = {N, 1, d.n_heads, k, 1, num_clusters,
+                           plan ? (int)plan_words_upper_bound(num_clusters, N) : 0};
   SelectParams p = {static_cast<const __nv_bfloat16*>(q_lat), static_cast<const __nv_bfloat16*>(q_rope),
                     static_cast<const int8_t*>(codes), scales, block_table, seq_lens, scores, sel_table, sel_lens,
-                    sel_pages, status, d.s_q, d.causal, d.n_heads, d.max_blocks_per_seq, d.num_blocks, k, n_first,
+                    sel_pages, status, plan, shape, N, d.s_q, d.causal, d.n_heads, d.max_blocks_per_seq, d.num_blocks, k, n_first,
                     n_recent};
-  const int N = d.B * d.s_q;
   cudaError_t e = cudaSuccess;
   if (d.max_blocks_per_seq > k && k > n_first + n_recent) {   // some row may have pages to choose from
     int dev = 0, sms = 0;
@@ -542,7 +643,7 @@ mla_status_t launch_select_pages(const mla_dims_t& d, const void* q_lat, const v
     if (e == cudaSuccess)
       e = launch_pdl(score_pages_kernel, dim3(N, runs), dim3(kScoreThreads), kScoreSmem, stream, p);
   }
-  if (e == cudaSuccess) e = launch_pdl(select_pages_kernel, dim3(N), dim3(kSelThreads), 0, stream, p);
+  if (e == cudaSuccess) e = launch_pdl(select_pages_kernel, dim3(plan ? N + 1 : N), dim3(kSelThreads), 0, stream, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return set_error(MLA_ERR_CUDA, "select_pages launch: %s", cudaGetErrorString(e));
   return MLA_OK;

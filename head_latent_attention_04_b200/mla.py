@@ -66,7 +66,8 @@ for _name, _args in {
     "mla_build_tables": [_i32, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
     "mla_plan_device": [_pdims, _vp, _i32, _vp, _sz, _vp, _vp],
     "mla_summarize_pages": [_vp, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp],
-    "mla_select_pages": [_pdims, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp],
+    "mla_select_pages": [_pdims, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp,
+                         _vp],
     "mla_combine": [_pdims, _vp, _vp, _vp, _vp, _vp, _vp],
     "mla_debug_gather_pages": [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp],
     "mla_decode_attn_combine_noalloc": [_pdims, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i32, _vp, _vp, _vp, _vp],
@@ -461,14 +462,17 @@ def summarize_pages(kv_pool, blocks, codes, scales, kv_cache: str = "bf16", stat
 
 
 def select_pages(dims: MlaDims, q_lat, q_rope, codes, scales, block_table, seq_lens, k: int, scores, sel_table,
-                 sel_lens, sel_pages=None, n_first: int = 1, n_recent: int = 1, status=None, stream=None):
+                 sel_lens, sel_pages=None, n_first: int = 1, n_recent: int = 1, status=None, stream=None,
+                 plan_dev=None, num_clusters: int = 0):
     """The pages each query row attends to: all of its pages if there are at most
     ``k``, else the first ``n_first``, the last ``n_recent`` and the best scores.
     Writes ``sel_table`` int32 [N][k] (a block table with one row per query),
-    ``sel_lens`` int32 [N] and, if given, ``sel_pages`` int32 [N][k]."""
+    ``sel_lens`` int32 [N] and, if given, ``sel_pages`` int32 [N][k] and
+    ``plan_dev`` (the plan of the selection for ``num_clusters`` clusters)."""
     N, H = dims.B * dims.s_q, dims.n_heads
     i32 = torch.int32
-    with _on(q_lat, q_rope, codes, scales, block_table, seq_lens, scores, sel_table, sel_lens, sel_pages, status):
+    with _on(q_lat, q_rope, codes, scales, block_table, seq_lens, scores, sel_table, sel_lens, sel_pages, plan_dev,
+             status):
         _check(_lib.mla_select_pages(
             ctypes.byref(dims), _arg(q_lat, "q_lat", torch.bfloat16, N, H, 512),
             _arg(q_rope, "q_rope", torch.bfloat16, N, H, 64), _arg(codes, "codes", torch.int8, dims.num_blocks, 576),
@@ -476,8 +480,9 @@ def select_pages(dims: MlaDims, q_lat, q_rope, codes, scales, block_table, seq_l
             _arg(block_table, "block_table", i32, dims.B, dims.max_blocks_per_seq),
             _arg(seq_lens, "seq_lens", i32, dims.B), k, n_first, n_recent,
             _arg(scores, "scores", torch.float32, N, dims.max_blocks_per_seq), _arg(sel_table, "sel_table", i32, N, k),
-            _arg(sel_lens, "sel_lens", i32, N), _arg(sel_pages, "sel_pages", i32, N, k), _vec(status, "status", torch.int32),
-            _stream(stream)), "mla_select_pages")
+            _arg(sel_lens, "sel_lens", i32, N), _arg(sel_pages, "sel_pages", i32, N, k), num_clusters,
+            _vec(plan_dev, "plan_dev", i32), 0 if plan_dev is None else 4 * plan_dev.numel(),
+            _vec(status, "status", i32), _stream(stream)), "mla_select_pages")
     return sel_table, sel_lens, sel_pages
 
 
@@ -668,8 +673,8 @@ class SparseOutputs:
 
 class SparseAttention:
     """Attention of each query over the pages a cheap score picks, for one batch
-    shape: :func:`select_pages`, :func:`plan_device` of the selection, the decode
-    kernel of the cache's kind and :func:`combine`.
+    shape: :func:`select_pages` (which makes the plan of its selection too), the
+    decode kernel of the cache's kind and :func:`combine`.
 
     Lengths stay on the device, so one captured ``run()`` serves a batch as it
     grows, and rows of length 0 (a padded batch) are left as they were.  The
@@ -698,21 +703,37 @@ class SparseAttention:
         self.o_lat = new(N, n_heads, 512, dtype=torch.bfloat16)
         self.lse = new(N, n_heads, dtype=torch.float32)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._out = SparseOutputs(self.o_lat, self.lse, self.pages, self.table, self.lens, self.status)
+        # the arguments of the three calls that stay the same from run to run
+        self._attn = {"bf16": _lib.mla_decode_attn, "fp8": _lib.mla_decode_attn_fp8cache,
+                      "fp4": _lib.mla_decode_attn_fp4cache}[kv_cache]
+        at = lambda t: t.data_ptr()
+        self._refs = ctypes.byref(self.dims), ctypes.byref(self.row_dims)
+        self._selection = (k, n_first, n_recent, at(self.scores), at(self.table), at(self.lens), at(self.pages),
+                           self.num_clusters, at(self.plan_dev), plan_bytes, at(self.status))
+        self._attention = (at(self.table), at(self.lens), at(self.plan_dev), self.num_clusters, at(self.o_part),
+                           at(self.lse_part), at(self.o_lat), at(self.lse), at(self.status))
+        self._merge = at(self.plan_dev), at(self.o_part), at(self.lse_part), at(self.o_lat), at(self.lse)
 
     def run(self, q_lat, q_rope, kv_pool, codes, scales, block_table, seq_lens, stream=None) -> SparseOutputs:
         """``codes`` and ``scales``: the summaries of the pool's full pages
-        (:func:`summarize_pages`); ``seq_lens`` int32 [B] on the device."""
-        select_pages(self.dims, q_lat, q_rope, codes, scales, block_table, seq_lens, self.k, self.scores, self.table,
-                     self.lens, self.pages, self.n_first, self.n_recent, self.status, stream)
-        plan_device(self.row_dims, self.lens, self.num_clusters, self.plan_dev, self.status, stream)
+        (:func:`summarize_pages`); ``seq_lens`` int32 [B] on the device.  The outputs are the
+        object's own buffers."""
+        d = self.dims
+        N, H, nb = d.B * d.s_q, d.n_heads, d.num_blocks
         dtype, row = _POOL_ROWS[self.kv_cache]
-        _arg(kv_pool, "kv_pool", dtype, self.dims.num_blocks, 64, row)
-        attn = {"bf16": decode_attn, "fp8": decode_attn_fp8cache, "fp4": decode_attn_fp4cache}[self.kv_cache]
-        with _on(kv_pool, q_lat):
-            attn(self.row_dims, q_lat, q_rope, kv_pool, self.table, self.lens, self.plan_dev, self.num_clusters,
-                 self.o_part, self.lse_part, self.o_lat, self.lse, self.status, stream)
-            combine(self.row_dims, self.plan_dev, self.o_part, self.lse_part, self.o_lat, self.lse, stream)
-        return SparseOutputs(self.o_lat, self.lse, self.pages, self.table, self.lens, self.status)
+        with _on(self.o_lat, q_lat, q_rope, kv_pool, codes, scales, block_table, seq_lens):
+            s = _stream(stream)
+            queries = _arg(q_lat, "q_lat", torch.bfloat16, N, H, 512), _arg(q_rope, "q_rope", torch.bfloat16, N, H, 64)
+            pool = _arg(kv_pool, "kv_pool", dtype, nb, 64, row)
+            whole, rows = self._refs
+            _check(_lib.mla_select_pages(
+                whole, *queries, _arg(codes, "codes", torch.int8, nb, 576), _arg(scales, "scales", torch.float32, nb),
+                _arg(block_table, "block_table", torch.int32, d.B, d.max_blocks_per_seq),
+                _arg(seq_lens, "seq_lens", torch.int32, d.B), *self._selection, s), "mla_select_pages")
+            _check(self._attn(rows, *queries, pool, *self._attention, s), "attention over the selection")
+            _check(_lib.mla_combine(rows, *self._merge, s), "mla_combine")
+        return self._out
 
 
 class GraphedStep:

@@ -407,17 +407,21 @@ mla_status_t mla_plan_device(const mla_dims_t* dims, const int32_t* seq_lens, in
  *   sel_lens  int32 [N], written: the tokens in them that the row sees (the last page is always
  *             chosen, so only it can be partly filled)
  *   sel_pages int32 [N][k] or NULL, written: the pages' numbers, -1 behind the last
+ *   plan_dev  device buffer or NULL, written: the plan of sel_lens for num_clusters clusters
+ *             (mla_plan_size with B = N, s_q = 1, max_blocks_per_seq = k; dims->causal = 1), made
+ *             beside the selection.  num_clusters and plan_bytes count only with it
  *   status    MLA_STATUS_BAD_SEQLEN: a length below s_q or beyond the table (the row selects nothing);
  *             MLA_STATUS_BAD_BLOCK: a scored page's block lies outside the pool (scored -inf)
- * The attention then takes dims with B = N, s_q = 1 and max_blocks_per_seq = k,
- * sel_table, sel_lens and a plan of sel_lens (mla_plan_device).  Queries must be finite.
+ * The attention then takes dims with B = N, s_q = 1, causal = 1 and
+ * max_blocks_per_seq = k, sel_table, sel_lens and that plan.  Queries must be finite.
  */
 mla_status_t mla_summarize_pages(const void* kv_pool, int32_t cache, const int32_t* blocks, int32_t n,
                                  int32_t num_blocks, void* codes, float* scales, int32_t* status, void* stream);
 mla_status_t mla_select_pages(const mla_dims_t* dims, const void* q_lat, const void* q_rope, const void* codes,
                               const float* scales, const int32_t* block_table, const int32_t* seq_lens, int32_t k,
                               int32_t n_first, int32_t n_recent, float* scores, int32_t* sel_table,
-                              int32_t* sel_lens, int32_t* sel_pages, int32_t* status, void* stream);
+                              int32_t* sel_lens, int32_t* sel_pages, int32_t num_clusters, void* plan_dev,
+                              size_t plan_bytes, int32_t* status, void* stream);
 
 /*
  * mla_combine -- log-sum-exp merge of the split pieces of each split row:

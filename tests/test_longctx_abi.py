@@ -90,7 +90,7 @@ def test_summary_and_selection_arguments():
     refused(1, "mla_summarize_pages", A, 0, A, 2, 8, A + 8, A, None, None)
     refused(1, "mla_summarize_pages", A, 0, A, 2, 8, A, None, None, None)
     d = dims()
-    good = [ctypes.byref(d), A, A, A, A, A, A, 3, 1, 1, A, A, A, A, None, None]
+    good = [ctypes.byref(d), A, A, A, A, A, A, 3, 1, 1, A, A, A, A, 74, A, 1 << 20, None, None]
     def bad(i, v, code=1):
         args = list(good)
         args[i] = v
@@ -104,6 +104,10 @@ def test_summary_and_selection_arguments():
     bad(7, 1 << 26, 2)
     bad(8, -1)
     bad(9, 0)
+    bad(14, 0)
+    bad(14, 4097)
+    bad(15, A + 2)
+    bad(16, 64, 3)
 
 
 def test_python_side_refuses_types_shapes_and_devices():
