@@ -36,66 +36,44 @@ __device__ __forceinline__ void report(int32_t* status, int bits) {
   if (status) atomicOr(status, bits);
 }
 
-__global__ void __launch_bounds__(kThreads)
-kv_quantize_fp4_kernel(const uint4* __restrict__ kv, const int32_t* __restrict__ slots, long long n,
-                       uint8_t* __restrict__ pool, long long pool_rows, int32_t* status) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int c = threadIdx.x % kRowChunks;
-  const long long row = (long long)blockIdx.x * kRowsPerBlock + threadIdx.x / kRowChunks;
-  // (no early return: the four threads of a group share a row, so a shuffle
-  // needs only the threads of its own group, which all take the same way)
-  const bool in = row < n;
-  const long long slot = in ? (long long)slots[row] : -1;
-  const bool live = slot >= 0 && slot < pool_rows;
-  if (in && !live && slot != -1 && c == 0) report(status, MLA_STATUS_BAD_BLOCK);
-  const uint4 v = live ? __ldg(kv + row * kRowChunks + c) : make_uint4(0, 0, 0, 0);
+// One thread's part of a row: 8 columns of c_KV, or 16 bytes of k_rope (c >= kLatChunks).
+// `live` is the same for the four threads of a group.
+__device__ __forceinline__ void quantize_chunk(uint4 v, int c, bool live, uint8_t* dst, int32_t* status) {
   float x[8];
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = 0;   // largest magnitudes, a pair of bf16 (their signs come out meaningless)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(w[i] << 16);
     x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
   }
-  float amax = 0.f;
-  bool nan = false;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    amax = fmaxf(amax, fabsf(x[i]));
-    nan |= x[i] != x[i];
-  }
+  m = max(m & 0x7FFFu, (m >> 16) & 0x7FFFu);   // (as integers magnitudes order like the values, NaN above all)
   const uint32_t group = 0xFu << (threadIdx.x & 28);   // the lanes of this group of 32 columns
-  amax = fmaxf(amax, __shfl_xor_sync(group, amax, 1));
-  amax = fmaxf(amax, __shfl_xor_sync(group, amax, 2));
-  nan = __any_sync(group, nan);
+  m = max(m, __shfl_xor_sync(group, m, 1));
+  m = max(m, __shfl_xor_sync(group, m, 2));
   if (!live) return;
-  uint8_t* dst = pool + slot * kF4Row;
   if (c >= kLatChunks) {
     reinterpret_cast<uint4*>(dst + kF4RopeOff)[c - kLatChunks] = v;
     return;
   }
-  // The largest usable scale: beyond it 6 s leaves fp16.  Such a row is written
-  // with that scale and flagged.
-  __half s16 = __float2half_rn(fminf(amax, 65504.f) / 6.f);
-  bool out_of_range = nan;
-  if (!(__half2float(s16) <= kF4MaxScale)) {
-    s16 = __float2half_rn(kF4MaxScale);
-    out_of_range = true;
-  }
-  if (amax > 65504.f) out_of_range = true;
+  // The largest usable scale: beyond it 6 s leaves fp16.  A group with a larger value or a
+  // NaN is written with that scale and flagged.
+  const float amax = __uint_as_float(m << 16);
+  const bool out_of_range = !(amax <= 65504.f);
+  const __half s16 = __float2half_rn(out_of_range ? kF4MaxScale : amax / 6.f);
   const float s = __half2float(s16);
   const float r = s > 0.f ? 1.f / s : 0.f;
-  // y = x / s is within 2^-22 of the quotient (relative).  A quotient that is not
-  // half-way between two grid values is at least 2^-13 away from it (x has 8
-  // significant bits, s 11, a half-way point 3), and |y| < 8.5 unless the row is
-  // flagged, so adding and taking off 48 (a grid of 2^-18) moves only the exact
-  // ties, onto the tie: the codes are those of the exact quotient.
+  // x r is within 2^-22 of x / s (relative).  A quotient that is not half-way
+  // between two grid values is at least 2^-13 away from it (x has 8 significant bits,
+  // s 11, a half-way point 3), and |x / s| < 8.5 unless the row is flagged, so
+  // adding and taking off 48 (a grid of 2^-18) moves only the exact ties, onto the
+  // tie: the codes are those of the exact quotient.
   uint32_t codes = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float y0 = __fsub_rn(__fadd_rn(x[2 * i] * r, 48.f), 48.f);
-    const float y1 = __fsub_rn(__fadd_rn(x[2 * i + 1] * r, 48.f), 48.f);
-    codes |= cvt_e2m1x2(copysignf(y0, x[2 * i]), copysignf(y1, x[2 * i + 1])) << (8 * i);
+    const float y0 = __fsub_rn(__fmaf_rn(x[2 * i], r, 48.f), 48.f), y1 = __fsub_rn(__fmaf_rn(x[2 * i + 1], r, 48.f), 48.f);
+    codes |= cvt_e2m1x2(y0, y1) << (8 * i);
   }
   reinterpret_cast<uint32_t*>(dst)[c] = codes;
   if ((c & 3) == 0) {
@@ -104,37 +82,94 @@ kv_quantize_fp4_kernel(const uint4* __restrict__ kv, const int32_t* __restrict__
   }
 }
 
+// kRows rows per thread, all loads in flight before the first is used: rows
+// blockIdx.x * 4 kRows + 4 i + threadIdx.x / 72.
+template <int kRows>
+__global__ void __launch_bounds__(kThreads)
+kv_quantize_fp4_kernel(const uint4* __restrict__ kv, const int32_t* __restrict__ slots, long long n,
+                       uint8_t* __restrict__ pool, long long pool_rows, int32_t* status) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int c = threadIdx.x % kRowChunks;
+  const long long row0 = (long long)blockIdx.x * (kRowsPerBlock * kRows) + threadIdx.x / kRowChunks;
+  uint4 v[kRows];
+  long long slot[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const long long row = row0 + kRowsPerBlock * i;
+    slot[i] = row < n ? (long long)slots[row] : -1;
+    v[i] = row < n ? __ldg(kv + row * kRowChunks + c) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    // (no early return: the shuffles of a group's four threads, which share a row)
+    const bool live = slot[i] >= 0 && slot[i] < pool_rows;
+    if (!live && slot[i] != -1 && c == 0) report(status, MLA_STATUS_BAD_BLOCK);
+    quantize_chunk(v[i], c, live, pool + slot[i] * kF4Row, status);
+  }
+}
+
+template <int kRows>
 __global__ void __launch_bounds__(kThreads)
 kv_dequantize_fp4_kernel(const uint8_t* __restrict__ pool, const int32_t* __restrict__ slots, long long n,
                          uint4* __restrict__ out, long long pool_rows, int32_t* status) {
   griddep_wait();
   griddep_launch_dependents();
   const int c = threadIdx.x % kRowChunks;
-  const long long row = (long long)blockIdx.x * kRowsPerBlock + threadIdx.x / kRowChunks;
-  if (row >= n) return;
-  const long long slot = slots[row];
-  if (slot < 0 || slot >= pool_rows) {
-    if (slot != -1 && c == 0) report(status, MLA_STATUS_BAD_BLOCK);
-    return;
-  }
-  const uint8_t* src = pool + slot * kF4Row;
-  if (c >= kLatChunks) {
-    out[row * kRowChunks + c] = __ldg(reinterpret_cast<const uint4*>(src + kF4RopeOff) + (c - kLatChunks));
-    return;
-  }
-  const uint32_t codes = __ldg(reinterpret_cast<const uint32_t*>(src) + c);
-  const float s = __half2float(__ldg(reinterpret_cast<const __half*>(src + kF4ScaleOff) + (c >> 2)));
-  uint32_t o[4];
+  const long long row0 = (long long)blockIdx.x * (kRowsPerBlock * kRows) + threadIdx.x / kRowChunks;
+  long long slot[kRows];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {   // code x scale is exact in fp32 (2 + 11 bits); one rounding to bf16
-    const float2 f = unpack_f16x2(cvt_f16x2_e2m1x2((codes >> (8 * i)) & 0xFFu));
-    o[i] = pack_bf16(f.x * s, f.y * s);
+  for (int i = 0; i < kRows; ++i) {
+    const long long row = row0 + kRowsPerBlock * i;
+    slot[i] = row < n ? (long long)slots[row] : -1;
+    if (slot[i] < 0 || slot[i] >= pool_rows) {
+      if (slot[i] != -1 && c == 0) report(status, MLA_STATUS_BAD_BLOCK);
+      slot[i] = -1;
+    }
   }
-  out[row * kRowChunks + c] = make_uint4(o[0], o[1], o[2], o[3]);
+  if (c >= kLatChunks) {
+    uint4 v[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (slot[i] >= 0) v[i] = __ldg(reinterpret_cast<const uint4*>(pool + slot[i] * kF4Row + kF4RopeOff) + (c - kLatChunks));
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (slot[i] >= 0) out[(row0 + kRowsPerBlock * i) * kRowChunks + c] = v[i];
+    return;
+  }
+  uint32_t codes[kRows];
+  __half scale[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (slot[i] < 0) continue;
+    const uint8_t* src = pool + slot[i] * kF4Row;
+    codes[i] = __ldg(reinterpret_cast<const uint32_t*>(src) + c);
+    scale[i] = __ldg(reinterpret_cast<const __half*>(src + kF4ScaleOff) + (c >> 2));
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (slot[i] < 0) continue;
+    const float s = __half2float(scale[i]);
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {   // code x scale is exact in fp32 (2 + 11 bits); one rounding to bf16
+      const float2 f = unpack_f16x2(cvt_f16x2_e2m1x2((codes[i] >> (8 * k)) & 0xFFu));
+      o[k] = pack_bf16(f.x * s, f.y * s);
+    }
+    out[(row0 + kRowsPerBlock * i) * kRowChunks + c] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
 }
 
-mla_status_t grid_of(long long n, unsigned* blocks) {
-  const long long g = (n + kRowsPerBlock - 1) / kRowsPerBlock;
+// Rows per thread: one while the blocks of that fit the card at once (a step's
+// rows: latency counts), else four (a prompt's: bytes in flight count).
+mla_status_t grid_of(long long n, bool* many, unsigned* blocks) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return set_error(MLA_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
+  *many = n > (long long)sms * (2048 / kThreads) * kRowsPerBlock;
+  const long long per = *many ? 4 * kRowsPerBlock : kRowsPerBlock;
+  const long long g = (n + per - 1) / per;
   if (g > INT32_MAX) return set_error(MLA_ERR_UNSUPPORTED, "too many rows in one call");
   *blocks = (unsigned)g;
   return MLA_OK;
@@ -144,10 +179,11 @@ mla_status_t grid_of(long long n, unsigned* blocks) {
 
 mla_status_t launch_kv_quantize_fp4(const void* kv, const int32_t* slots, long long n, void* pool_fp4,
                                     long long pool_rows, int32_t* status, void* stream) {
+  bool many = false;
   unsigned blocks = 0;
-  mla_status_t st = grid_of(n, &blocks);
+  mla_status_t st = grid_of(n, &many, &blocks);
   if (st != MLA_OK) return st;
-  cudaError_t e = launch_pdl(kv_quantize_fp4_kernel, dim3(blocks), dim3(kThreads), 0, stream,
+  cudaError_t e = launch_pdl(many ? kv_quantize_fp4_kernel<4> : kv_quantize_fp4_kernel<1>, dim3(blocks), dim3(kThreads), 0, stream,
                              static_cast<const uint4*>(kv), slots, n, static_cast<uint8_t*>(pool_fp4), pool_rows,
                              status);
   if (e == cudaSuccess) e = cudaGetLastError();
@@ -157,10 +193,11 @@ mla_status_t launch_kv_quantize_fp4(const void* kv, const int32_t* slots, long l
 
 mla_status_t launch_kv_dequantize_fp4(const void* pool_fp4, const int32_t* slots, long long n, void* out,
                                       long long pool_rows, int32_t* status, void* stream) {
+  bool many = false;
   unsigned blocks = 0;
-  mla_status_t st = grid_of(n, &blocks);
+  mla_status_t st = grid_of(n, &many, &blocks);
   if (st != MLA_OK) return st;
-  cudaError_t e = launch_pdl(kv_dequantize_fp4_kernel, dim3(blocks), dim3(kThreads), 0, stream,
+  cudaError_t e = launch_pdl(many ? kv_dequantize_fp4_kernel<4> : kv_dequantize_fp4_kernel<1>, dim3(blocks), dim3(kThreads), 0, stream,
                              static_cast<const uint8_t*>(pool_fp4), slots, n, static_cast<uint4*>(out), pool_rows,
                              status);
   if (e == cudaSuccess) e = cudaGetLastError();

@@ -88,23 +88,47 @@ build_tables_kernel(const TablesParams p) {
       p.seq_lens[b] = admitted ? old + add : max(old, 0);
     }
     __syncthreads();
-    for (int e = t; e < pages_now; e += kThreads) {
-      const int i = find_owner(s_pages, kThreads, e);
-      const int rank = e - (i > 0 ? s_pages[i - 1] : 0);
-      const int blk = p.free_blocks[used + e];
-      if (blk < 0 || blk >= p.num_blocks) report(p.status, MLA_STATUS_BAD_BLOCK);
-      p.table[(size_t)(b0 + i) * p.max_blocks + s_held[i] + rank] = blk;
+    // Pages, then tokens: one each per thread, or four neighbours when there are more
+    // than threads, so that a search finds the request of the first and the
+    // others' follow by stepping on.
+    const int per_p = pages_now > kThreads ? 4 : 1;
+    for (int e0 = t * per_p; e0 < pages_now; e0 += kThreads * per_p) {
+      int i = find_owner(s_pages, kThreads, e0);
+      int blk[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) blk[u] = u < per_p && e0 + u < pages_now ? p.free_blocks[used + e0 + u] : -1;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int e = e0 + u;
+        if (u >= per_p || e >= pages_now) break;
+        while (s_pages[i] <= e) ++i;
+        if (blk[u] < 0 || blk[u] >= p.num_blocks) report(p.status, MLA_STATUS_BAD_BLOCK);
+        p.table[(size_t)(b0 + i) * p.max_blocks + s_held[i] + e - (i > 0 ? s_pages[i - 1] : 0)] = blk[u];
+      }
     }
     __syncthreads();   // the new table entries are read below
     if (p.fill) {
-      for (int e = t; e < tokens_now; e += kThreads) {
-        const int i = find_owner(s_tokens, kThreads, e);
-        const int pos = s_cached[i] + e - (i > 0 ? s_tokens[i - 1] : 0);
-        const int blk = __ldcg(p.table + (size_t)(b0 + i) * p.max_blocks + pos / kPage);
-        const bool ok = blk >= 0 && blk < p.num_blocks;
-        if (!ok) report(p.status, MLA_STATUS_BAD_BLOCK);
-        p.slots[tokens_before + e] = ok ? blk * kPage + pos % kPage : -1;
-        if (p.positions) p.positions[tokens_before + e] = pos;
+      const int per_t = tokens_now > kThreads ? 4 : 1;
+      for (int e0 = t * per_t; e0 < tokens_now; e0 += kThreads * per_t) {
+        int i = find_owner(s_tokens, kThreads, e0);
+        int blk[4], pos[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int e = e0 + u;
+          if (u >= per_t || e >= tokens_now) break;
+          while (s_tokens[i] <= e) ++i;
+          pos[u] = s_cached[i] + e - (i > 0 ? s_tokens[i - 1] : 0);
+          blk[u] = __ldcg(p.table + (size_t)(b0 + i) * p.max_blocks + pos[u] / kPage);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int e = e0 + u;
+          if (u >= per_t || e >= tokens_now) break;
+          const bool ok = blk[u] >= 0 && blk[u] < p.num_blocks;
+          if (!ok) report(p.status, MLA_STATUS_BAD_BLOCK);
+          p.slots[tokens_before + e] = ok ? blk[u] * kPage + pos[u] % kPage : -1;
+          if (p.positions) p.positions[tokens_before + e] = pos[u];
+        }
       }
     }
     pages_before += pages_all;
