@@ -407,19 +407,26 @@ def build_tables(cached_lens, new_lens, block_table, free_blocks, free_head, max
     request order.  ``out.seq_lens`` may be ``cached_lens`` and
     ``out.free_head`` may be ``free_head``: a captured step then moves on by itself.
     """
-    B = cached_lens.shape[0]
-    if out is None:
-        out = BatchTables.empty(B, max_new, cached_lens.device)
+    B, width = cached_lens.shape[0], block_table.shape[-1]
     i32 = torch.int32
-    with _on(cached_lens, new_lens, block_table, free_blocks, free_head, out.seq_lens, out.cu_new, out.slots,
-             out.positions, out.free_head, status):
+    if out is None:
+        out = BatchTables.empty(B, max_new, block_table.device)
+        at = out.seq_lens.data_ptr()              # the five arrays of empty(), one behind the other
+        lens, cu, slots, positions = at, at + 4 * B, at + 8 * B + 4, at + 8 * B + 4 + 4 * max_new
+        head_out = positions + 4 * max_new
+        device = _on(block_table, cached_lens, new_lens, free_blocks, free_head, status)
+    else:
+        lens, cu = _arg(out.seq_lens, "seq_lens", i32, B), _arg(out.cu_new, "cu_new", i32, B + 1)
+        slots, positions = _arg(out.slots, "slots", i32, max_new), _arg(out.positions, "positions", i32, max_new)
+        head_out = _arg(out.free_head, "free_head", i32, 1)
+        device = _on(block_table, cached_lens, new_lens, free_blocks, free_head, status, out.seq_lens, out.cu_new,
+                     out.slots, out.positions, out.free_head)
+    with device:
         _check(_lib.mla_build_tables(
-            B, _arg(cached_lens, "cached_lens", i32, B), _arg(new_lens, "new_lens", i32, B), block_table.shape[1],
-            _arg(block_table, "block_table", i32, B, block_table.shape[1]), _vec(free_blocks, "free_blocks", i32),
-            free_blocks.numel(), _arg(free_head, "free_head", i32, 1), num_blocks, max_new,
-            _arg(out.seq_lens, "seq_lens", i32, B), _arg(out.cu_new, "cu_new", i32, B + 1),
-            _arg(out.slots, "slots", i32, max_new), _arg(out.positions, "positions", i32, max_new),
-            _arg(out.free_head, "free_head", i32, 1), _vec(status, "status", torch.int32), _stream(stream)), "mla_build_tables")
+            B, _arg(cached_lens, "cached_lens", i32, B), _arg(new_lens, "new_lens", i32, B), width,
+            _arg(block_table, "block_table", i32, B, width), _vec(free_blocks, "free_blocks", i32), free_blocks.numel(),
+            _arg(free_head, "free_head", i32, 1), num_blocks, max_new, lens, cu, slots, positions, head_out,
+            _vec(status, "status", i32), _stream(stream)), "mla_build_tables")
     return out
 
 
