@@ -66,9 +66,10 @@ def parse_args(argv=None):
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--projections", default="bf16", choices=["bf16", "fp8"],
                     help="absorb / out_uv as bf16 GEMMs or as FP8 (E4M3) block-quantised BMMs")
-    ap.add_argument("--cache", default="bf16", choices=["bf16", "fp8"],
-                    help="latent cache rows as bf16 (1152 B/token) or E4M3 codes with fp32 block scales "
-                         "and a bf16 k_rope (656 B/token)")
+    ap.add_argument("--cache", default="bf16", choices=["bf16", "fp8", "fp4"],
+                    help="latent cache rows as bf16 (1152 B/token), E4M3 codes with fp32 block scales "
+                         "and a bf16 k_rope (656 B/token), or E2M1 codes with fp16 group scales and a bf16 "
+                         "k_rope (416 B/token)")
     ap.add_argument("--cpu-seconds", type=float, default=12.0, help="target CPU time of the oracle sample")
     ap.add_argument("--path", default="decode", choices=["decode", "prefill", "upstream", "spec"],
                     help="decode: the absorbed decode step (the headline line); prefill: order-1 prefill of one "
@@ -88,7 +89,8 @@ def algorithmic(seq_lens, s_q, H, causal=True, weight_bytes=2, cache_row_bytes=1
     Per attended (query, key) pair: 2*h*(2*d_c + d_R) FLOPs (QK over 576 +
     PV over 512 per head).  Per cached token: one cache row, read once and
     shared by all heads and all s_q query tokens of its sequence: 576 bf16 =
-    1152 B, or 656 B for the FP8 cache (512 E4M3 codes, 4 fp32 scales, 64 bf16).
+    1152 B, or 656 B for the FP8 cache (512 E4M3 codes, 4 fp32 scales, 64 bf16),
+    or 416 B for the 4-bit cache (512 E2M1 codes, 16 fp16 scales, 64 bf16).
     ``weight_bytes``: bytes per W_UK / W_UV element (1 for E4M3 codes, whose
     scales add 4 bytes per 128 x 128 block).
     """
@@ -353,19 +355,19 @@ def run_ours(args, rank: int, world: int, local_rank: int):
     preset = W.PRESETS[args.config]
     w = W.preset_workload(args.config, device=dev, seed=dp.replica_seed(preset.seed, rank))
     fp8 = args.projections == "fp8"
-    fp8_cache = args.cache == "fp8"
+    fp8_cache, fp4_cache = args.cache == "fp8", args.cache == "fp4"
     acc = algorithmic(w.seq_lens, w.s_q, w.n_heads, weight_bytes=1 if fp8 else 2,
-                      cache_row_bytes=mla.FP8_ROW_BYTES if fp8_cache else 1152)
+                      cache_row_bytes={"bf16": 1152, "fp8": mla.FP8_ROW_BYTES, "fp4": mla.FP4_ROW_BYTES}[args.cache])
     bt = torch.as_tensor(w.block_table, device=dev)
     dec = mla.Decoder(w.seq_lens, w.s_q, w.n_heads, w.max_blocks, w.num_blocks, dev, kv_cache=args.cache)
     if fp8:   # weights quantised once, outside the timed region (static, as the weights are)
         dec.use_fp8_projections(w.w_uk, w.w_uv)
-    if fp8_cache:   # the cache written once in FP8 (as a serving loop writes each new row), then resident
-        pool = mla.fp8_pool_from(w.kv_pool)
+    if fp8_cache or fp4_cache:   # the cache written once (as a serving loop writes each new row), then resident
+        pool = (mla.fp8_pool_from if fp8_cache else mla.fp4_pool_from)(w.kv_pool)
         torch.cuda.synchronize()
     else:
         pool = w.kv_pool
-    attn_fn = mla.decode_attn_fp8cache if fp8_cache else mla.decode_attn
+    attn_fn = {"bf16": mla.decode_attn, "fp8": mla.decode_attn_fp8cache, "fp4": mla.decode_attn_fp4cache}[args.cache]
     flush = torch.empty(L2_FLUSH_BYTES // 4, dtype=torch.float32, device=dev)
     stream = torch.cuda.current_stream(dev)
 
@@ -520,8 +522,8 @@ def run_ours(args, rank: int, world: int, local_rank: int):
         achieved = acc["attn_bytes"] / (attn * 1e-3) / 1e9
         roof = {"bound": "hbm", "achieved": achieved, "peak": peaks["hbm_gbs"], "unit": "GB/s",
                 "frac": achieved / peaks["hbm_gbs"]}
-    roof.update({"traffic": recorded_traffic(args.config + ("_fp8cache" if fp8_cache else "")),
-                 "kernel": "mla_decode_kernel" + ("<fp8 cache>" if fp8_cache else ""),
+    roof.update({"traffic": None if fp4_cache else recorded_traffic(args.config + ("_fp8cache" if fp8_cache else "")),
+                 "kernel": "mla_decode_fp4_kernel" if fp4_cache else "mla_decode_kernel" + ("<fp8 cache>" if fp8_cache else ""),
                  "alg_bytes_per_launch": acc["attn_bytes"], "alg_flops_per_launch": acc["attn_flops"],
                  "kernel_ms": attn, "peak_source": f"{peak_src} ({'MEASURED_PEAKS.json' if peak_src == 'measured' else 'recipe fallback'}, burst)"})
     step_roof_s = max(acc["step_bytes"] / (peaks["hbm_gbs"] * 1e9), acc["step_flops"] / (peaks["bf16_tflops"] * 1e12))
@@ -531,9 +533,11 @@ def run_ours(args, rank: int, world: int, local_rank: int):
         "steps": K, "warmup": args.warmup, "ms_per_step": ms, "higher_is_better": True,
         "scaling": "weak", "vs_baseline": None,
         "dtype": ("bf16 (attention" + ("; the latent cache stored as e4m3 codes with fp32 block scales, "
-                                       "widened to bf16 on chip" if fp8_cache else "") + ")"
-                  + ("; e4m3 codes with fp32 block scales (projections)" if fp8 else "")) if (fp8 or fp8_cache)
-                 else "bf16",
+                                       "widened to bf16 on chip" if fp8_cache else
+                                       "; the latent cache stored as e2m1 codes with fp16 group scales, "
+                                       "widened to fp16 on chip" if fp4_cache else "") + ")"
+                  + ("; e4m3 codes with fp32 block scales (projections)" if fp8 else ""))
+                 if (fp8 or fp8_cache or fp4_cache) else "bf16",
         "data": "synthetic",
         "config": dict(workload_config(args.config, w), parallelism=f"dp{world} (independent replicas)",
                        num_clusters=dec.num_clusters, split_slots=dec.num_slots,

@@ -1,8 +1,55 @@
-// Absorbed MLA decode attention over a 4-bit latent cache (fp4_format.h rows) on sm_100a.
+// Absorbed MLA decode attention over a 4-bit latent cache (rows of fp4_format.h)
+// on sm_100a: tcgen05, TMEM, TMA and 2-CTA clusters.
 //
-// The mathematics is that of decode_attn.cu: per query row (token n, head h),
+// The mathematics is that of decode_attn.cu, per query row (token n, head h) over keys t < kv_len:
 //   logit_t = scale * (q_lat . c_KV[t] + q_rope . k_rope[t]),  o_lat = sum_t softmax(logit)_t c_KV[t],
-// with c_KV[t, j] = code[t, j] * s[t, j / 32].
+// with c_KV[t, j] = code[t, j] * s[t, j / 32], one pass over the keys with a running
+// reference maximum and sum, and partial results merged by mla_combine where the plan
+// splits a row.
+//
+// What bounds it.  A token is 416 bytes, so at 128 heads its 2 x 128 x 1088 operations
+// take 2.7 times as long at the measured tensor rate as its bytes at the measured copy
+// rate: the floor is the tensor cores' (4 x 128K tokens: 89 us).  The scales vary
+// along both products' reduction or output axes (a key's groups along q_lat . c_KV, keys along
+// P . c_KV), so no product can run on the 4-bit codes: every half page is
+// widened to fp16 in shared memory.  The kernel runs at the power limit of the
+// card (about 950 W, the SM clock at 1.75 of 1.965 GHz when launched back to back) and at
+// about 2400 to 2600 cycles per 64-key page and cluster, of which the tensor
+// pipe needs 1088.  4 x 128K tokens: 176 us in bursts, 180 us launched back to
+// back for a second; the bf16 cache's kernel takes 157 and 183, the FP8 cache's 174 and 189
+// in the same loops.  So the 4-bit cache holds 2.8 times the tokens at the speed of the others.
+//
+// Why this shape (as in decode_attn.cu).  O for 128 heads x 512 columns in fp32 is
+// one SM's whole tensor memory, so a cluster of two CTAs splits the latent
+// dimension: CTA r owns latent columns [256r, 256r + 256) and RoPE columns [32r, 32r + 32),
+// computes partial scores over its 288 columns and exchanges them through
+// distributed shared memory in log2 units, rounded to fp16 (16 KB per page
+// each way, one bulk copy counted on the receiver's mbarrier); both CTAs add
+// fp16(S0) + fp16(S1), bit-identical in the pair.  The rounding moves a logit by at most
+// 2^-11 of a partial's size, below the bf16 rounding of the output.
+//
+// Two rings, because the cache's bytes are few: four raw half pages (13 KB each:
+// 8 KB of codes, 1 KB of scales, 4 KB of RoPE columns, which the QK product reads there)
+// hide the TMA's latency, and a stage of 32 KB holds the widened page from its QK to its PV product.
+// A single ring widened in place, as for the FP8 cache, holds its stage for the TMA's
+// latency too.
+//
+// TMEM (512 columns): O [0, 256) fp32, S [256, 320) fp32 (free once the sender has read
+// it), two P buffers [320, 352) and [352, 384) in fp16 (page g uses buffer g & 1),
+// q_lat half [384, 512) in fp16 pairs.
+//
+// Warps (512 threads): 0 TMA; 1 QK issuer, owner of the tensor memory; 2 PV issuer;
+// 3-6 query loader, widening and score sender (one thread per row); 7-14 softmax, correction, epilogue
+// (two warps per TMEM lane quarter, one per 32-key half); 15 copies score tiles to the peer.
+// Measured and not kept (4 x 128K tokens): four more warps for the widening alone 181 us
+// against 160 (each SM sub-partition then runs five warps whose chains slow one
+// another down); two softmax groups taking pages in turn with one thread per row
+// 198 us; two tiles for the peer's scores, no change; one wait for two barriers at once 181 to
+// 262 us; codes widened by byte permutes instead of the conversion instruction 203 us.
+//
+// Failure: every wait is bounded (200 ms by default, mla_set_wait_limit_ns); a role that
+// gives up sets MLA_STATUS_TIMEOUT, stops its peer, drains the copies and products it
+// issued and returns without trapping.
 #include "fp4_format.h"
 #include "mla_internal.h"
 #include "plan_format.h"
