@@ -41,12 +41,15 @@ __device__ __forceinline__ void report(int32_t* status, int bits) {
 
 // ---------------------------------------------------------------- summaries
 // One block per page: thread = (8 columns, 16 of the 64 rows), partial sums
-// joined through shared memory.  Bound by reading the page; the widening to
-// fp64 is done on the bits (the conversion instruction runs at a quarter of the
-// rate of the integer operations that replace it): the exponent and mantissa of
-// a bf16, fp16 or E2M1 value placed in a double's fields without correcting the
-// bias read as the value times a power of two, subnormals included.  All kinds
-// end in units of 2^896.
+// joined through shared memory.  The floor is reading the page (8192 pages: bf16 92 us, FP8
+// 52, 4-bit 33 at the measured copy rate); it takes 106, 102 and 75 us, the smaller rows
+// because what a value costs after it is read weighs more.  So the widening to fp64 is done
+// on the bits: the exponent and mantissa of a bf16, fp16 or E2M1 value placed in a
+// double's fields without correcting the bias read as the value times a power of two,
+// subnormals included (all kinds end in units of 2^896), and the 4-bit rows are summed in
+// fp32 where that is exact.  (8192 4-bit pages: 128 us with every product in fp64, 108 with
+// fp32 sums, 88 with eight rows' codes in registers at a time and one division per
+// thread, 75 with k_rope in a warp of its own and four blocks per SM.)
 constexpr int kSumThreads = kRowChunks * 4;
 
 enum class Cache { kBf16, kFp8, kFp4 };
@@ -65,7 +68,7 @@ __device__ __forceinline__ void add_bf16x8(const uint4& v, double (&acc)[8]) {
 }
 
 template <Cache kind>
-__global__ void __launch_bounds__(kSumThreads)
+__global__ void __launch_bounds__(kSumThreads, 4)
 summarize_pages_kernel(const uint8_t* __restrict__ pool, const int32_t* __restrict__ blocks, int num_blocks,
                        int8_t* __restrict__ codes, float* __restrict__ scales, int32_t* status) {
   constexpr int kRowBytes = kind == Cache::kBf16 ? 1152 : kind == Cache::kFp8 ? kF8Row : kF4Row;
@@ -80,7 +83,9 @@ summarize_pages_kernel(const uint8_t* __restrict__ pool, const int32_t* __restri
     if (blk != -1 && threadIdx.x == 0) report(status, MLA_STATUS_BAD_BLOCK);
     return;
   }
-  const int c = threadIdx.x % kRowChunks, part = threadIdx.x / kRowChunks;
+  // eight warps take c_KV (chunks 0 .. 63), the ninth k_rope (64 .. 71): no warp has both
+  const int t = threadIdx.x;
+  const int c = t < 256 ? t % 64 : 64 + t % 8, part = t < 256 ? t / 64 : (t - 256) / 8;
   const uint8_t* row = pool + ((size_t)blk * kPage + part * kRows) * kRowBytes;
   double acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (kind == Cache::kBf16 || c >= 64) {
@@ -103,44 +108,91 @@ summarize_pages_kernel(const uint8_t* __restrict__ pool, const int32_t* __restri
       }
     }
   } else {
-#pragma unroll 8
-    for (int r = 0; r < kRows; ++r) {
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(row + r * kRowBytes) + c);
-      const uint32_t h = __ldg(reinterpret_cast<const uint16_t*>(row + r * kRowBytes + kF4ScaleOff) + (c >> 2));
-      // fp16 scale x 2^(112 - 1008), then x 2^1022: the product below is then in units of 2^896
-      const double sd = from_hi((h & 0x7FFFu) << 10) * 0x1p1000 * 0x1p134;
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(row) + c;
+    uint32_t h[kRows], top = 0, low = 31;   // the rows' fp16 scales, their largest and smallest exponent
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t sign = (i == 7 ? w : w << (28 - 4 * i)) & 0x80000000u;
-        const uint32_t mag = (4 * i <= 19 ? w << (19 - 4 * i) : w >> (4 * i - 19)) & 0x00380000u;
-        acc[i] += sd * from_hi(sign | mag);
+    for (int r = 0; r < kRows; ++r)
+      h[r] = __ldg(reinterpret_cast<const uint16_t*>(row + r * kRowBytes + kF4ScaleOff) + (c >> 2));
+    uint32_t w[kRows / 2];                  // eight rows' codes at a time
+#pragma unroll
+    for (int r = 0; r < kRows / 2; ++r) w[r] = __ldg(src + r * (kF4Row / 4));
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      top = max(top, h[r] >> 10);
+      if (h[r] != 0) low = min(low, h[r] >> 10);
+    }
+    if (low >= 1 && top <= 30 && top - low <= 5) {
+      // Normal scales within 2^5 of one another, nearly always: code x scale is a multiple
+      // of 2^(low - 26) and 16 of them stay below 2^(top - 7), 24 bits apart at most, so
+      // fp32 sums of the exact products are exact.
+      float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const uint32_t codes8 = w[r % (kRows / 2)];
+        if (r < kRows / 2) w[r] = __ldg(src + (r + kRows / 2) * (kF4Row / 4));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t x = cvt_f16x2_e2m1x2((codes8 >> (8 * k)) & 0xFFu);
+          asm("{\n\t.reg .f16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+              "fma.rn.f32.f16 %0, lo, %3, %0;\n\tfma.rn.f32.f16 %1, hi, %3, %1;\n\t}"
+              : "+f"(f[2 * k]), "+f"(f[2 * k + 1])
+              : "r"(x), "h"((uint16_t)h[r]));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = (double)f[i] * 0x1p-896;
+    } else {
+#pragma unroll 1
+      for (int r = 0; r < kRows; ++r) {
+        const uint32_t codes8 = __ldg(src + r * (kF4Row / 4));
+        const uint32_t scale = __ldg(reinterpret_cast<const uint16_t*>(row + r * kRowBytes + kF4ScaleOff) + (c >> 2));
+        // fp16 scale x 2^-1008, then x 2^1134: times the codes' 2^-1022 the product is in units of 2^896
+        const double sd = from_hi((scale & 0x7FFFu) << 10) * 0x1p1000 * 0x1p134;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t sign = (i == 7 ? codes8 : codes8 << (28 - 4 * i)) & 0x80000000u;
+          const uint32_t mag = (4 * i <= 19 ? codes8 << (19 - 4 * i) : codes8 >> (4 * i - 19)) & 0x00380000u;
+          acc[i] += sd * from_hi(sign | mag);
+        }
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; i += 2)
-    *reinterpret_cast<double2*>(&s_sum[part][8 * c + i]) = make_double2(acc[i], acc[i + 1]);
+  for (int k = 0; k < 4; ++k) {   // (neighbours start at different pairs: fewer bank conflicts)
+    const int i = (k + c) & 3;
+    const double2 v = i == 0   ? make_double2(acc[0], acc[1])
+                      : i == 1 ? make_double2(acc[2], acc[3])
+                      : i == 2 ? make_double2(acc[4], acc[5])
+                               : make_double2(acc[6], acc[7]);
+    *reinterpret_cast<double2*>(&s_sum[part][8 * c + 2 * i]) = v;
+  }
   __syncthreads();
   const int col = 2 * threadIdx.x;
   double sum[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     sum[i] = (s_sum[0][col + i] + s_sum[1][col + i]) + (s_sum[2][col + i] + s_sum[3][col + i]);
-  // (magnitudes of doubles compare as integers)
-  unsigned long long m = max((unsigned long long)__double_as_longlong(fabs(sum[0])),
-                             (unsigned long long)__double_as_longlong(fabs(sum[1])));
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x / 32] = m;
+  // (magnitudes of doubles compare as integers: high words, then low words of the highest)
+  const double big = fabs(sum[0]) > fabs(sum[1]) ? fabs(sum[0]) : fabs(sum[1]);
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)__double2hiint(big));
+  const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)__double2hiint(big) == hi ? (uint32_t)__double2loint(big) : 0u);
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x / 32] = (unsigned long long)hi << 32 | lo;
   __syncthreads();
-  m = s_max[0];
+  unsigned long long m = s_max[0];
 #pragma unroll
   for (int i = 1; i < kSumThreads / 32; ++i) m = max(m, s_max[i]);
   const double amax = __longlong_as_double((long long)m);
   int q[2] = {0, 0};
   if (amax > 0.0) {
+    // rint(127 sum / amax) by a multiplication, good to 2^-44 absolute; closer than 2^-40 to
+    // half-way the quotient itself decides
+    const double r = 127.0 / amax;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) q[i] = __double2int_rn(sum[i] * 127.0 / amax);
+    for (int i = 0; i < 2; ++i) {
+      const double y = sum[i] * r;
+      q[i] = __double2int_rn(y);
+      if (fabs(fabs(y - (double)q[i]) - 0.5) < 0x1p-40) q[i] = __double2int_rn(sum[i] * 127.0 / amax);
+    }
   }
   reinterpret_cast<char2*>(codes + (size_t)blk * kDim)[threadIdx.x] = make_char2((signed char)q[0], (signed char)q[1]);
   if (threadIdx.x == 0) scales[blk] = (float)(amax * 0x1p890 / 127.0);   // 2^896 / 64

@@ -62,6 +62,25 @@ def test_summaries_are_exact(mla, kind, nb):
     np.testing.assert_array_equal(scales.cpu().numpy(), want_scales)
 
 
+@pytest.mark.parametrize("spread", [4, 5, 6, 12, 24])
+def test_fp4_summaries_of_scales_far_apart(mla, spread):
+    """Rows whose scales differ by up to 2^spread: up to 2^5 within 16 rows the sums are kept in fp32,
+    beyond in fp64; zero and subnormal scales among them."""
+    nb = 40
+    pool = drifting_pool(nb, spread).float()
+    g = torch.Generator().manual_seed(spread)
+    pool[..., :512] *= 2.0 ** (-torch.randint(0, spread + 1, (nb, 64, 1), generator=g).float())
+    pool[3, 5:9] = 0
+    pool[4, 17, :64] *= 2.0 ** -20
+    p, values = pool_of_kind(mla, pool.to(torch.bfloat16), "fp4")
+    codes = torch.zeros((nb, 576), dtype=torch.int8, device=DEV)
+    scales = torch.zeros((nb,), device=DEV)
+    mla.summarize_pages(p, torch.arange(nb, dtype=torch.int32, device=DEV), codes, scales, "fp4")
+    want_codes, want_scales = summaries(values)
+    np.testing.assert_array_equal(codes.cpu().numpy(), want_codes)
+    np.testing.assert_array_equal(scales.cpu().numpy(), want_scales)
+
+
 def test_summary_ties_skips_and_bad_blocks(mla):
     pool = torch.zeros((4, 64, 576))
     pool[2, :, 0], pool[2, :, 1], pool[2, :, 2] = 2.0, 1.0, -1.0      # 63.5 goes to 64
