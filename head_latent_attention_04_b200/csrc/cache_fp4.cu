@@ -15,7 +15,8 @@
 // and 416 out per row (and the reverse).  A thread owns 8 columns (16 bytes of
 // bf16, 4 bytes of codes), 72 threads a row, so that every load and store of a
 // warp is contiguous; the four threads of a group combine their maxima by
-// shuffles.
+// shuffles.  Reads go to L2 (__ldcg): the kernel before, whose end this one waits for
+// after its blocks have started, may have written what is read.
 #include "fp4_format.h"
 #include "mla_internal.h"
 #include "ptx.cuh"
@@ -86,8 +87,8 @@ __device__ __forceinline__ void quantize_chunk(uint4 v, int c, bool live, uint8_
 // blockIdx.x * 4 kRows + 4 i + threadIdx.x / 72.
 template <int kRows>
 __global__ void __launch_bounds__(kThreads)
-kv_quantize_fp4_kernel(const uint4* __restrict__ kv, const int32_t* __restrict__ slots, long long n,
-                       uint8_t* __restrict__ pool, long long pool_rows, int32_t* status) {
+kv_quantize_fp4_kernel(const uint4* kv, const int32_t* slots, long long n,
+                       uint8_t* pool, long long pool_rows, int32_t* status) {
   griddep_wait();
   griddep_launch_dependents();
   const int c = threadIdx.x % kRowChunks;
@@ -97,8 +98,8 @@ kv_quantize_fp4_kernel(const uint4* __restrict__ kv, const int32_t* __restrict__
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const long long row = row0 + kRowsPerBlock * i;
-    slot[i] = row < n ? (long long)slots[row] : -1;
-    v[i] = row < n ? __ldg(kv + row * kRowChunks + c) : make_uint4(0, 0, 0, 0);
+    slot[i] = row < n ? (long long)__ldcg(slots + row) : -1;
+    v[i] = row < n ? __ldcg(kv + row * kRowChunks + c) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
@@ -111,8 +112,8 @@ kv_quantize_fp4_kernel(const uint4* __restrict__ kv, const int32_t* __restrict__
 
 template <int kRows>
 __global__ void __launch_bounds__(kThreads)
-kv_dequantize_fp4_kernel(const uint8_t* __restrict__ pool, const int32_t* __restrict__ slots, long long n,
-                         uint4* __restrict__ out, long long pool_rows, int32_t* status) {
+kv_dequantize_fp4_kernel(const uint8_t* pool, const int32_t* slots, long long n,
+                         uint4* out, long long pool_rows, int32_t* status) {
   griddep_wait();
   griddep_launch_dependents();
   const int c = threadIdx.x % kRowChunks;
@@ -121,7 +122,7 @@ kv_dequantize_fp4_kernel(const uint8_t* __restrict__ pool, const int32_t* __rest
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const long long row = row0 + kRowsPerBlock * i;
-    slot[i] = row < n ? (long long)slots[row] : -1;
+    slot[i] = row < n ? (long long)__ldcg(slots + row) : -1;
     if (slot[i] < 0 || slot[i] >= pool_rows) {
       if (slot[i] != -1 && c == 0) report(status, MLA_STATUS_BAD_BLOCK);
       slot[i] = -1;
@@ -131,7 +132,7 @@ kv_dequantize_fp4_kernel(const uint8_t* __restrict__ pool, const int32_t* __rest
     uint4 v[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
-      if (slot[i] >= 0) v[i] = __ldg(reinterpret_cast<const uint4*>(pool + slot[i] * kF4Row + kF4RopeOff) + (c - kLatChunks));
+      if (slot[i] >= 0) v[i] = __ldcg(reinterpret_cast<const uint4*>(pool + slot[i] * kF4Row + kF4RopeOff) + (c - kLatChunks));
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
       if (slot[i] >= 0) out[(row0 + kRowsPerBlock * i) * kRowChunks + c] = v[i];
@@ -143,8 +144,8 @@ kv_dequantize_fp4_kernel(const uint8_t* __restrict__ pool, const int32_t* __rest
   for (int i = 0; i < kRows; ++i) {
     if (slot[i] < 0) continue;
     const uint8_t* src = pool + slot[i] * kF4Row;
-    codes[i] = __ldg(reinterpret_cast<const uint32_t*>(src) + c);
-    scale[i] = __ldg(reinterpret_cast<const __half*>(src + kF4ScaleOff) + (c >> 2));
+    codes[i] = __ldcg(reinterpret_cast<const uint32_t*>(src) + c);
+    scale[i] = __ldcg(reinterpret_cast<const __half*>(src + kF4ScaleOff) + (c >> 2));
   }
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {

@@ -381,7 +381,7 @@ mla_status_t mla_build_tables(int32_t B, const int32_t* cached_lens, const int32
   clear_error();
   if (B < 1 || max_blocks_per_seq < 1 || n_free < 0 || num_blocks < 1 || max_new < 0)
     return set_error(MLA_ERR_INVALID_ARG, "B, max_blocks_per_seq and num_blocks must be >= 1, n_free and max_new >= 0");
-  if (B > 65536) return set_error(MLA_ERR_UNSUPPORTED, "more than 65536 requests");
+  if (B > 65536 || max_new > (1 << 30)) return set_error(MLA_ERR_UNSUPPORTED, "more than 65536 requests or 2^30 tokens");
   if ((int64_t)max_blocks_per_seq * 64 > INT32_MAX - 64 || (int64_t)num_blocks * 64 > INT32_MAX)
     return set_error(MLA_ERR_UNSUPPORTED, "max_blocks_per_seq or num_blocks too large");
   MLA_TRY(check_words(cached_lens, "cached_lens"));

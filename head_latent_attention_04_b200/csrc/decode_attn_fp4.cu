@@ -289,7 +289,8 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
                        plan[kHdrNumRows] == p.n_rows && plan[kHdrHeads] == p.n_heads &&
                        plan[kHdrB] == p.B && plan[kHdrSq] == p.s_q &&
                        plan[kHdrMaxBlocks] == p.max_blocks && plan[kHdrCausal] == (p.causal ? 1 : 0) &&
-                       plan[kHdrOffCluster] == off_cluster && plan[kHdrOffItems] == off_items;
+                       plan[kHdrOffCluster] == off_cluster && plan[kHdrOffItems] == off_items &&
+                       (plan[kHdrNumSlots] == 0 || (p.o_part != nullptr && p.lse_part != nullptr));
   const int it_begin = plan_ok ? it_begin_raw : 0;
   const int it_end = plan_ok ? it_end_raw : 0;
   if (!plan_ok && threadIdx.x == 0 && rank == 0 && cid == 0) report(p.status, MLA_STATUS_BAD_PLAN);
@@ -511,7 +512,7 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
           // (the 64-byte swizzle the MMA descriptor names)
           uint4 q[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) q[k] = r < p.n_heads ? __ldg(rsrc + k) : make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < 4; ++k) q[k] = r < p.n_heads ? __ldcg(rsrc + k) : make_uint4(0, 0, 0, 0);
           const uint32_t dst = smem_u32(s_qrope) + r * 64;
 #pragma unroll
           for (int k = 0; k < 4; ++k) st_shared_v4(dst + ((k ^ ((r >> 1) & 3)) << 4), q[k]);
@@ -525,7 +526,7 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
           uint32_t v[32];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const uint4 q = r < p.n_heads ? __ldg(src + 8 * hq + k) : make_uint4(0, 0, 0, 0);
+            const uint4 q = r < p.n_heads ? __ldcg(src + 8 * hq + k) : make_uint4(0, 0, 0, 0);
             v[4 * k] = bf16x2_to_f16x2(q.x); v[4 * k + 1] = bf16x2_to_f16x2(q.y);
             v[4 * k + 2] = bf16x2_to_f16x2(q.z); v[4 * k + 3] = bf16x2_to_f16x2(q.w);
           }

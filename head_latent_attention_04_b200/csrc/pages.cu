@@ -69,8 +69,8 @@ __device__ __forceinline__ void add_bf16x8(const uint4& v, double (&acc)[8]) {
 
 template <Cache kind>
 __global__ void __launch_bounds__(kSumThreads, 4)
-summarize_pages_kernel(const uint8_t* __restrict__ pool, const int32_t* __restrict__ blocks, int num_blocks,
-                       int8_t* __restrict__ codes, float* __restrict__ scales, int32_t* status) {
+summarize_pages_kernel(const uint8_t* pool, const int32_t* blocks, int num_blocks,
+                       int8_t* codes, float* scales, int32_t* status) {
   constexpr int kRowBytes = kind == Cache::kBf16 ? 1152 : kind == Cache::kFp8 ? kF8Row : kF4Row;
   constexpr int kRope = kind == Cache::kBf16 ? 1024 : kind == Cache::kFp8 ? kF8RopeOff : kF4RopeOff;
   constexpr int kRows = kPage / 4;
@@ -91,12 +91,12 @@ summarize_pages_kernel(const uint8_t* __restrict__ pool, const int32_t* __restri
   if (kind == Cache::kBf16 || c >= 64) {
     const uint8_t* src = kind == Cache::kBf16 ? row + 16 * c : row + kRope + 16 * (c - 64);
 #pragma unroll 8
-    for (int r = 0; r < kRows; ++r) add_bf16x8(__ldg(reinterpret_cast<const uint4*>(src + r * kRowBytes)), acc);
+    for (int r = 0; r < kRows; ++r) add_bf16x8(__ldcg(reinterpret_cast<const uint4*>(src + r * kRowBytes)), acc);
   } else if (kind == Cache::kFp8) {
 #pragma unroll 8
     for (int r = 0; r < kRows; ++r) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + r * kRowBytes) + c);
-      const float s = __ldg(reinterpret_cast<const float*>(row + r * kRowBytes + kF8ScaleOff) + (c >> 4));
+      const uint2 v = __ldcg(reinterpret_cast<const uint2*>(row + r * kRowBytes) + c);
+      const float s = __ldcg(reinterpret_cast<const float*>(row + r * kRowBytes + kF8ScaleOff) + (c >> 4));
       const double sd = (double)s * 0x1p112;
       uint32_t h[4];
       dequant_e4m3x4_f16(v.x, 0x3C003C00u, h[0], h[1]);   // codes as fp16 (times 1), exact
@@ -112,10 +112,10 @@ summarize_pages_kernel(const uint8_t* __restrict__ pool, const int32_t* __restri
     uint32_t h[kRows], top = 0, low = 31;   // the rows' fp16 scales, their largest and smallest exponent
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
-      h[r] = __ldg(reinterpret_cast<const uint16_t*>(row + r * kRowBytes + kF4ScaleOff) + (c >> 2));
+      h[r] = __ldcg(reinterpret_cast<const uint16_t*>(row + r * kRowBytes + kF4ScaleOff) + (c >> 2));
     uint32_t w[kRows / 2];                  // eight rows' codes at a time
 #pragma unroll
-    for (int r = 0; r < kRows / 2; ++r) w[r] = __ldg(src + r * (kF4Row / 4));
+    for (int r = 0; r < kRows / 2; ++r) w[r] = __ldcg(src + r * (kF4Row / 4));
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       top = max(top, h[r] >> 10);
@@ -129,7 +129,7 @@ summarize_pages_kernel(const uint8_t* __restrict__ pool, const int32_t* __restri
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
         const uint32_t codes8 = w[r % (kRows / 2)];
-        if (r < kRows / 2) w[r] = __ldg(src + (r + kRows / 2) * (kF4Row / 4));
+        if (r < kRows / 2) w[r] = __ldcg(src + (r + kRows / 2) * (kF4Row / 4));
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint32_t x = cvt_f16x2_e2m1x2((codes8 >> (8 * k)) & 0xFFu);
@@ -144,8 +144,8 @@ summarize_pages_kernel(const uint8_t* __restrict__ pool, const int32_t* __restri
     } else {
 #pragma unroll 1
       for (int r = 0; r < kRows; ++r) {
-        const uint32_t codes8 = __ldg(src + r * (kF4Row / 4));
-        const uint32_t scale = __ldg(reinterpret_cast<const uint16_t*>(row + r * kRowBytes + kF4ScaleOff) + (c >> 2));
+        const uint32_t codes8 = __ldcg(src + r * (kF4Row / 4));
+        const uint32_t scale = __ldcg(reinterpret_cast<const uint16_t*>(row + r * kRowBytes + kF4ScaleOff) + (c >> 2));
         // fp16 scale x 2^-1008, then x 2^1134: times the codes' 2^-1022 the product is in units of 2^896
         const double sd = from_hi((scale & 0x7FFFu) << 10) * 0x1p1000 * 0x1p134;
 #pragma unroll
@@ -356,7 +356,7 @@ score_pages_kernel(const SelectParams p) {
         report(p.status, MLA_STATUS_BAD_BLOCK);
         id = -1;
       }
-      if (id >= 0) scale = __ldg(p.scales + id);
+      if (id >= 0) scale = __ldcg(p.scales + id);
     }
     // chunks 0 .. 31 of row j go through lanes 0 .. 31, the last four of all eight rows together
     const uint32_t a = a_addr + b * kOperandBytes;
@@ -405,9 +405,9 @@ score_pages_kernel(const SelectParams p) {
       const size_t at = (size_t)n * p.n_heads + 8 * warp + j;
       const bool in = 8 * warp + j < p.n_heads;
       const uint4 zero = make_uint4(0, 0, 0, 0);
-      v[j][0] = in ? __ldg(reinterpret_cast<const uint4*>(p.q_lat + at * 512) + lane) : zero;
-      v[j][1] = in ? __ldg(reinterpret_cast<const uint4*>(p.q_lat + at * 512) + 32 + lane) : zero;
-      v[j][2] = in && lane < 8 ? __ldg(reinterpret_cast<const uint4*>(p.q_rope + at * 64) + lane) : zero;
+      v[j][0] = in ? __ldcg(reinterpret_cast<const uint4*>(p.q_lat + at * 512) + lane) : zero;
+      v[j][1] = in ? __ldcg(reinterpret_cast<const uint4*>(p.q_lat + at * 512) + 32 + lane) : zero;
+      v[j][2] = in && lane < 8 ? __ldcg(reinterpret_cast<const uint4*>(p.q_rope + at * 64) + lane) : zero;
     }
     scale[0] = gather(tile, 0, id_next);
     id_next = tile + step < tiles ? read_id(tile + step) : -1;

@@ -159,6 +159,14 @@ def _on(*tensors):
     return _SAME_DEVICE if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
+def _made_on(stream):
+    """Context in which a call's own tensors are made: on the stream that the call
+    uses, so that their memory and their fills belong to it."""
+    if stream is None:
+        return _SAME_DEVICE
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+
 def _stream(stream=None) -> int:
     if stream is None:
         if _raw_stream is not None:
@@ -365,7 +373,8 @@ def kv_dequantize_fp4(kv_pool_fp4, slots, kv=None, status=None, stream=None):
     bad slots are left as they were; zeros when ``kv`` is made here)."""
     nb, n = kv_pool_fp4.shape[0], slots.shape[0]
     if kv is None:
-        kv = torch.zeros((n, 576), dtype=torch.bfloat16, device=kv_pool_fp4.device)
+        with _made_on(stream):
+            kv = torch.zeros((n, 576), dtype=torch.bfloat16, device=kv_pool_fp4.device)
     with _on(kv_pool_fp4, kv, slots, status):
         _check(_lib.mla_kv_dequantize_fp4(_arg(kv_pool_fp4, "kv_pool_fp4", torch.uint8, nb, 64, FP4_ROW_BYTES),
                                           _arg(slots, "slots", torch.int32, n), n, _arg(kv, "kv", torch.bfloat16, n, 576),
@@ -377,8 +386,9 @@ def kv_dequantize_fp4(kv_pool_fp4, slots, kv=None, status=None, stream=None):
 def fp4_pool_from(kv_pool, stream=None):
     """The 4-bit copy of a whole bf16 pool [num_blocks][64][576] (every slot quantised)."""
     nb = kv_pool.shape[0]
-    pool4 = torch.empty((nb, 64, FP4_ROW_BYTES), dtype=torch.uint8, device=kv_pool.device)
-    slots = torch.arange(nb * 64, dtype=torch.int32, device=kv_pool.device)
+    with _made_on(stream):
+        pool4 = torch.empty((nb, 64, FP4_ROW_BYTES), dtype=torch.uint8, device=kv_pool.device)
+        slots = torch.arange(nb * 64, dtype=torch.int32, device=kv_pool.device)
     return kv_quantize_fp4(kv_pool.reshape(nb * 64, 576), slots, pool4, stream=stream)
 
 
@@ -410,7 +420,8 @@ def build_tables(cached_lens, new_lens, block_table, free_blocks, free_head, max
     B, width = cached_lens.shape[0], block_table.shape[-1]
     i32 = torch.int32
     if out is None:
-        out = BatchTables.empty(B, max_new, block_table.device)
+        with _made_on(stream):
+            out = BatchTables.empty(B, max_new, block_table.device)
         at = out.seq_lens.data_ptr()              # the five arrays of empty(), one behind the other
         lens, cu, slots, positions = at, at + 4 * B, at + 8 * B + 4, at + 8 * B + 4 + 4 * max_new
         head_out = positions + 4 * max_new
@@ -439,8 +450,8 @@ def plan_device(dims: MlaDims, seq_lens, num_clusters: int, plan_dev=None, statu
     """:func:`plan` made on the GPU from device ``seq_lens`` (int32 [B]; 0 is a
     padded row without work): the same words, as an int32 device tensor."""
     if plan_dev is None:
-        words = _plan_words(dims.B * dims.s_q, num_clusters)
-        plan_dev = torch.empty(words, dtype=torch.int32, device=seq_lens.device)
+        with _made_on(stream):
+            plan_dev = torch.empty(_plan_words(dims.B * dims.s_q, num_clusters), dtype=torch.int32, device=seq_lens.device)
     with _on(seq_lens, plan_dev, status):
         _check(_lib.mla_plan_device(ctypes.byref(dims), _arg(seq_lens, "seq_lens", torch.int32, dims.B), num_clusters,
                                     _vec(plan_dev, "plan_dev", torch.int32), 4 * plan_dev.numel(), _vec(status, "status", torch.int32),

@@ -300,7 +300,8 @@ mla_status_t mla_kv_quantize_fp8(const void* kv, const int32_t* slots, int64_t n
  * Numerics: rows are widened on chip to fp16 (code * scale, rounded once), q_lat is rounded to
  * fp16, P is written as fp16, and the products accumulate in fp32; the RoPE
  * products are bf16, and partial scores are exchanged in fp16 as in
- * mla_decode_attn.  |q_lat| <= 65504 (else MLA_STATUS_SCORE_RANGE).  All other
+ * mla_decode_attn.  |q_lat| <= 65504 (else MLA_STATUS_SCORE_RANGE).  A plan that splits a
+ * row without o_part and lse_part is MLA_STATUS_BAD_PLAN.  All other
  * arguments, outputs, status bits and the plan are those of mla_decode_attn;
  * mla_combine completes split rows.  No draft-tree masks.
  */
@@ -344,8 +345,9 @@ mla_status_t mla_kv_dequantize_fp4(const void* pool_fp4, const int32_t* slots, i
  *                 (the last one, when new tokens go into it), those of new pages are written,
  *                 all others stay
  *   free_blocks   int32 [n_free], free_head int32 [1]: the next free block is free_blocks[free_head[0]]
+ *                 (a head outside [0, n_free] is reported as NO_SPACE and counts as n_free)
  *   num_blocks    blocks in the pool (entries outside are reported)
- *   max_new       entries of slots and positions
+ *   max_new       entries of slots and positions, at most 2^30
  *   seq_lens      int32 [B], written: cached_lens + new_lens (may be cached_lens itself)
  *   cu_new        int32 [B + 1], written: new tokens before request b
  *   slots         int32 [max_new], written: block * 64 + row of each new token, requests in order;

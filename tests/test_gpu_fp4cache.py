@@ -149,6 +149,26 @@ def test_values_beyond_fp16_are_flagged_and_stay_finite(mla, value):
     assert status.item() == 0 and np.array_equal(pool.reshape(-1, ROW4)[:4].cpu().numpy()[:, 256:], pack_rows(kv)[:, 256:])
 
 
+def test_rows_written_and_read_back_at_once_many_times(mla):
+    """Every pass writes other values to the same slots and reads them back, with nothing between
+    the launches, on a stream of its own: the reader never sees the pass before."""
+    pool = torch.zeros((64, 64, ROW4), dtype=torch.uint8, device=DEV)
+    slots = torch.randperm(64 * 64, generator=torch.Generator().manual_seed(0))[:3000].to(torch.int32).to(DEV)
+    base = torch.randint(1, 7, (3000, 576), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for i in range(20):
+        with torch.cuda.stream(side):
+            kv = torch.where(base > 3, float(6 << i % 8), 0.0).to(torch.bfloat16) * (1 if i % 2 else -1)
+            kv[:, ::32] = float(6 << i % 8)                # every group reaches 6 x a power of two: exact
+        mla.kv_quantize_fp4(kv, slots, pool, stream=side)
+        got.append((kv, mla.kv_dequantize_fp4(pool, slots, stream=side)))
+    torch.cuda.synchronize()
+    for kv, back in got:
+        assert torch.equal(back, kv)
+
+
 def test_empty_calls(mla):
     pool = torch.zeros((1, 64, ROW4), dtype=torch.uint8, device=DEV)
     none = torch.zeros(0, dtype=torch.int32, device=DEV)
@@ -237,6 +257,42 @@ def test_bad_block_stale_length_and_wrong_plan_are_reported(mla):
     assert dec.status.item() & mla.STATUS_BAD_PLAN
     with pytest.raises(ValueError, match="bf16 cache"):
         dec.run(wd.q_nope, wd.q_rope, pool4, bt, wd.w_uk, wd.w_uv, draft_masks=bt)
+
+
+def test_a_plan_that_splits_rows_needs_the_workspaces(mla):
+    w = W.make_workload(1, 1, 16, [3000], seed=3, pool="permuted")
+    pool4 = oracle_pool(w).to(DEV)
+    dec = mla.Decoder(w.seq_lens, 1, 16, w.max_blocks, w.num_blocks, DEV, kv_cache="fp4")
+    assert dec.num_slots > 0
+    bt = torch.as_tensor(w.block_table, dtype=torch.int32, device=DEV)
+    q = torch.zeros((1, 16, 512), dtype=torch.bfloat16, device=DEV)
+    out = torch.full_like(q, 7.0)
+    for o_part, lse_part in ((None, None), (dec.o_part, None), (None, dec.lse_part)):
+        dec.status.zero_()
+        mla.decode_attn_fp4cache(dec.dims, q, q[..., :64].contiguous(), pool4, bt, dec.seq_lens_dev, dec.plan_dev,
+                                 dec.num_clusters, o_part, lse_part, out, status=dec.status)
+        assert dec.status.item() == mla.STATUS_BAD_PLAN and torch.all(out == 7.0)
+
+
+def test_graphed_and_streamed_steps_on_the_4_bit_cache(mla):
+    w = W.make_workload(3, 2, 32, [700, 64, 1000], seed=17, pool="permuted")
+    pool4 = oracle_pool(w)
+    dec, res = run_fp4(mla, w, pool4)
+    want = res.out.clone()
+    wd, pool = w.to(DEV), pool4.to(DEV)
+    for make in (mla.GraphedStep, mla.StreamedDecoder):
+        step = make(dec, pool, wd.w_uk, wd.w_uv)
+        if make is mla.GraphedStep:
+            step.q_nope.copy_(w.q_nope), step.q_rope.copy_(w.q_rope)
+            step.block_table.copy_(torch.as_tensor(w.block_table))
+            assert torch.equal(step.run(), want.cpu())
+        else:
+            for qn, qr, bt in step.host_in:
+                qn.copy_(w.q_nope), qr.copy_(w.q_rope), bt.copy_(torch.as_tensor(w.block_table))
+            ids = [step.submit() for _ in range(2)]
+            for i in ids:
+                assert torch.equal(step.wait(i), want.cpu())
+    assert dec.status.item() == 0
 
 
 def test_queries_beyond_fp16_are_reported(mla):

@@ -66,6 +66,7 @@ def test_build_tables_arguments():
         bad(i, -1)
     bad(0, 65537, 2)
     bad(3, 1 << 25, 2)
+    bad(9, (1 << 30) + 1, 2)
     bad(8, 1 << 26, 2)
     for i in (1, 2, 4, 5, 7, 10, 11, 12, 14):
         bad(i, None)
