@@ -12,12 +12,15 @@
 // rate: the floor is the tensor cores' (4 x 128K tokens: 89 us).  The scales vary
 // along both products' reduction or output axes (a key's groups along q_lat . c_KV, keys along
 // P . c_KV), so no product can run on the 4-bit codes: every half page is
-// widened to fp16 in shared memory.  The kernel runs at the power limit of the
-// card (about 950 W, the SM clock at 1.75 of 1.965 GHz when launched back to back) and at
-// about 2400 to 2600 cycles per 64-key page and cluster, of which the tensor
-// pipe needs 1088.  4 x 128K tokens: 176 us in bursts, 180 us launched back to
-// back for a second; the bf16 cache's kernel takes 157 and 183, the FP8 cache's 174 and 189
-// in the same loops.  So the 4-bit cache holds 2.8 times the tokens at the speed of the others.
+// widened to fp16 in shared memory.  No unit is saturated (tensor pipe 29 %, issue
+// slots 34 %, shared memory 40 % on 32 x 4096 tokens): the kernel is bound by the
+// serial chains of its warps.  The sender warps' turn per 64-key page (widen 880 cycles,
+// four waits of 200 to 450, conversion and store of the scores 450) and the softmax warps' (2400) set the pace, about
+// 2450 cycles, of which the tensor pipe needs 1088.  4 x 128K tokens: 148 us launched from a graph,
+// 173 us launched back to back for a second, where the card's power limit holds the SM
+// clock at 1.69 of 1.965 GHz; in that loop the bf16 cache's kernel takes 183 us, the FP8
+// cache's 188 (32 x 4096 tokens: 50 against 55 and 58).  So the 4-bit cache holds
+// 2.8 times the tokens of bf16 and is a little faster.
 //
 // Why this shape (as in decode_attn.cu).  O for 128 heads x 512 columns in fp32 is
 // one SM's whole tensor memory, so a cluster of two CTAs splits the latent
@@ -41,11 +44,17 @@
 // Warps (512 threads): 0 TMA; 1 QK issuer, owner of the tensor memory; 2 PV issuer;
 // 3-6 query loader, widening and score sender (one thread per row); 7-14 softmax, correction, epilogue
 // (two warps per TMEM lane quarter, one per 32-key half); 15 copies score tiles to the peer.
-// Measured and not kept (4 x 128K tokens): four more warps for the widening alone 181 us
-// against 160 (each SM sub-partition then runs five warps whose chains slow one
-// another down); two softmax groups taking pages in turn with one thread per row
-// 198 us; two tiles for the peer's scores, no change; one wait for two barriers at once 181 to
-// 262 us; codes widened by byte permutes instead of the conversion instruction 203 us.
+// Steps (4 x 128K tokens, from a graph): the widening in the sender warps with a ring of
+// its own for the raw pages 160 us; 16 loads of a row's query in flight 157; the wait for
+// the own tile before, not after, the scores are read 149 (it is over by then, and the
+// scores' registers are not live across it); the wait for a P buffer at the start
+// of a page 148.  Measured and not kept: four more warps for the widening alone 167 to 181 us (each SM
+// sub-partition then runs five warps whose chains slow one another down, and the softmax
+// warps set the pace); two softmax groups taking pages in turn with one thread per row
+// 198; two tiles for the peer's scores, no change; one wait for two barriers at
+// once 181 to 262; one lane waiting for its warp 480; test_wait before try_wait 157; codes widened by
+// byte permutes instead of the conversion instruction 203; queries read past L1
+// 6 us more per work item.
 //
 // Failure: every wait is bounded (200 ms by default, mla_set_wait_limit_ns); a role that
 // gives up sets MLA_STATUS_TIMEOUT, stops its peer, drains the copies and products it
@@ -142,8 +151,10 @@ __device__ __forceinline__ void report(int32_t* status, int bits) {
   if (status) atomicOr(status, bits);
 }
 
-// Suspend-time hint of the pipeline waits (0: no hint, spin).
-constexpr uint32_t kWaitHintNs = 200;
+// Suspend-time hint of the pipeline waits: a waiting warp takes no issue slots, and
+// the waits, which stand inlined in every role's loop, are half as long as without it
+// (4 x 128K tokens: 149 us against 165).
+constexpr uint32_t kWaitHintNs = 1000;
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile WaitCtl* wc) {
   return __all_sync(0xffffffffu, mbar_wait<false, kWaitHintNs>(bar, parity, wc));
@@ -478,9 +489,12 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
                    : "r"(raw + kRawScales + cr * 16 + ch * 8)
                    : "memory");
       const uint32_t row = smem_u32(s_kv + s * kStageBytes) + 2 * ch * kChunkBytes + cr * 128;
+      uint4 raw_codes[4];   // (all reads before the first write: their latencies overlap)
+#pragma unroll
+      for (int gi = 0; gi < 4; ++gi) raw_codes[gi] = ld_shared_v4(codes + (((4 * ch + gi) ^ (cr & 7)) << 4));
 #pragma unroll
       for (int gi = 0; gi < 4; ++gi) {
-        const uint4 v = ld_shared_v4(codes + (((4 * ch + gi) ^ (cr & 7)) << 4));
+        const uint4 v = raw_codes[gi];
         const uint32_t sc2 = __byte_perm(gi < 2 ? s01 : s23, 0, (gi & 1) ? 0x3232 : 0x1010);
         const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
         const uint32_t dst = row + (gi >> 1) * kChunkBytes;
@@ -512,7 +526,7 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
           // (the 64-byte swizzle the MMA descriptor names)
           uint4 q[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) q[k] = r < p.n_heads ? __ldcg(rsrc + k) : make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < 4; ++k) q[k] = r < p.n_heads ? rsrc[k] : make_uint4(0, 0, 0, 0);
           const uint32_t dst = smem_u32(s_qrope) + r * 64;
 #pragma unroll
           for (int k = 0; k < 4; ++k) st_shared_v4(dst + ((k ^ ((r >> 1) & 3)) << 4), q[k]);
@@ -520,17 +534,21 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
         }
         const uint4* src = reinterpret_cast<const uint4*>(p.q_lat + ((size_t)w[kItRow] * p.n_heads + r) * 512 +
                                                           256 * rank);
-        // the latent products take fp16 operands: 32 columns at a time
+        // the latent products take fp16 operands.  128 columns at a time: 16 loads in flight
+        // (plain loads: the eight pieces of a line that a row's thread reads one after
+        // the other come from L1; through L2 alone an item started 6 us later)
 #pragma unroll 1
-        for (int hq = 0; hq < 4; ++hq) {
-          uint32_t v[32];
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t v[64];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint4 q = r < p.n_heads ? __ldcg(src + 8 * hq + k) : make_uint4(0, 0, 0, 0);
-            v[4 * k] = bf16x2_to_f16x2(q.x); v[4 * k + 1] = bf16x2_to_f16x2(q.y);
-            v[4 * k + 2] = bf16x2_to_f16x2(q.z); v[4 * k + 3] = bf16x2_to_f16x2(q.w);
+          for (int k = 0; k < 16; ++k) {
+            const uint4 q = r < p.n_heads ? src[16 * hh + k] : make_uint4(0, 0, 0, 0);
+            v[4 * k] = q.x; v[4 * k + 1] = q.y; v[4 * k + 2] = q.z; v[4 * k + 3] = q.w;
           }
-          tmem_st32(tmem + lane_addr + kTmemQ + 32 * hq, v);
+#pragma unroll
+          for (int k = 0; k < 64; ++k) v[k] = bf16x2_to_f16x2(v[k]);
+          tmem_st32(tmem + lane_addr + kTmemQ + 64 * hh, *reinterpret_cast<uint32_t(*)[32]>(v));
+          tmem_st32(tmem + lane_addr + kTmemQ + 64 * hh + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
         }
         tmem_st_wait();
         tc_fence_before();
@@ -543,6 +561,8 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
         for (; widened < min(g + 2, pages_total); ++widened)
           if (!widen(widened)) goto sender_fail;
         uint32_t v[64];
+        // single tile: page g - 1's own tile must have been read by the softmax and the copy
+        if (g >= 1 && !warp_wait(&bars->own_free, (g - 1) & 1, wc)) goto sender_fail;
         if (!warp_wait(&bars->s_full, g & 1, wc)) goto sender_fail;
         tc_fence_after();
         tmem_ld32(tmem + lane_addr + kTmemS, *reinterpret_cast<uint32_t(*)[32]>(v));
@@ -555,8 +575,6 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
 #pragma unroll
         for (int k = 0; k < 32; ++k)   // scaled to log2 units, then rounded to fp16
           hv[k] = pack_f16(__uint_as_float(v[2 * k]) * sl2, __uint_as_float(v[2 * k + 1]) * sl2);
-        // single tile: page g - 1's own tile must have been read by the softmax and the copy
-        if (g >= 1 && !warp_wait(&bars->own_free, (g - 1) & 1, wc)) goto sender_fail;
         {
           uint8_t* own = s_xown + r * kXRow;
 #pragma unroll
@@ -639,6 +657,8 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
         const int gj = g + j, b = gj & 1;
         // full score = fp16(own partial) + fp16(peer partial), identical in both CTAs.
         // The own tile is read (and released) first: it lands before the peer's.
+        // P buffer gj & 1 is free once the PV product of page gj - 2 has completed
+        if (gj >= 2 && !warp_wait(&bars->o_full[gj & 1], ((gj >> 1) - 1) & 1, wc)) goto softmax_fail;
         uint4 po[4], pr[4];
         const uint32_t off_base = (uint32_t)(4 * c);
         if (!warp_wait(&bars->own_full, gj & 1, wc)) goto softmax_fail;
@@ -725,8 +745,6 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
         }
         l_run = l_run * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
 
-        // P buffer gj & 1 is free once the PV product of page gj - 2 has completed
-        if (gj >= 2 && !warp_wait(&bars->o_full[gj & 1], ((gj >> 1) - 1) & 1, wc)) goto softmax_fail;
         if (__any_sync(0xffffffffu, move && j > 0)) {
           // rescaling O: the PV product of page gj - 1 (same item) must have landed
           if (!warp_wait(&bars->o_full[(gj - 1) & 1], ((gj - 1) >> 1) & 1, wc)) goto softmax_fail;
