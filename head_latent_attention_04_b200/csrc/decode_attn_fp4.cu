@@ -94,9 +94,7 @@ constexpr int kOffKV = 0;
 constexpr int kOffRaw = kOffKV + kStages * kStageBytes;
 constexpr int kOffXPeer = kOffRaw + kRawStages * kRawBytes;  // peer's partial scores (one tile)
 constexpr int kOffXOwn = kOffXPeer + kXBytes;                // own partial scores (fp16, one tile)
-constexpr int kOffPMax = kOffXOwn + kXBytes;                 // fp32 [2 pages][2 halves][128] half-row maxima
-constexpr int kOffLSum = kOffPMax + 4 * kRows * 4;     // fp32 [2 items][2 halves][128] half-row sums
-constexpr int kOffQRope = kOffLSum + 4 * kRows * 4;    // bf16 q_rope half, 128 rows x 64 B (SW64, A of QK)
+constexpr int kOffQRope = kOffXOwn + kXBytes;                // bf16 q_rope half, 128 rows x 64 B (SW64, A of QK)
 constexpr int kOffBar = kOffQRope + kRows * 64;
 
 constexpr int kThreads = 512;            // 16 warps
@@ -139,8 +137,6 @@ struct Bars {
   uint64_t o_full[2];     // PV product of a page complete, per P buffer (page g uses buffer g & 1)
   uint64_t o_done;        // every PV product of the current item complete (epilogue)
   uint64_t o_free, qk_done, pv_done;
-  uint64_t pmax[2][4];   // the two softmax warps of row quarter q posted their page-b half-row maxima
-  uint64_t lsum[4];      // the two softmax warps of row quarter q posted their half-row sums (per item)
   uint32_t tmem_base;    // TMEM allocation
   uint32_t sent_count;   // score tiles this CTA has copied to its peer
   WaitCtl wc;            // abort flag and wait limit of every role
@@ -183,6 +179,44 @@ __device__ __forceinline__ int last_page_keys(const int32_t* w) {
   return w[kItKvLen] - (w[kItPageEnd] - 1) * kPage;
 }
 
+// Tensor-memory access of 16 lanes (taddr's lane .. + 15): threads 0-15 at taddr, threads 16-31
+// (the same lanes again) kSplit columns on; N consecutive columns each.
+template <int kSplit>
+__device__ __forceinline__ void tmem_ld16x2_32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32], %33;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr), "n"(kSplit));
+}
+template <int kSplit>
+__device__ __forceinline__ void tmem_st16x2_32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x32bx2.x32.b32 [%0], %1, "
+      "{%2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33};" ::"r"(taddr),
+      "n"(kSplit), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+template <int kSplit>
+__device__ __forceinline__ void tmem_st16x2_16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x32bx2.x16.b32 [%0], %1, "
+      "{%2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17};" ::"r"(taddr),
+      "n"(kSplit), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 // fp16 pair sum and maximum (round to nearest even; the maximum of -inf and x is x).
 __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -220,8 +254,6 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
   uint8_t* s_raw = smem + kOffRaw;
   uint8_t* s_xpeer = smem + kOffXPeer;
   uint8_t* s_xown = smem + kOffXOwn;
-  float* s_pmax = reinterpret_cast<float*>(smem + kOffPMax);
-  float* s_lsum = reinterpret_cast<float*>(smem + kOffLSum);
   uint8_t* s_qrope = smem + kOffQRope;
   Bars* bars = reinterpret_cast<Bars*>(smem + kOffBar);
   uint32_t* tmem_slot = &bars->tmem_base;
@@ -264,11 +296,6 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
     mbar_init(&bars->o_free, kSoftWarps);
     mbar_init(&bars->qk_done, 1);
     mbar_init(&bars->pv_done, 1);
-    for (int q = 0; q < 4; ++q) {
-      mbar_init(&bars->pmax[0][q], 2);
-      mbar_init(&bars->pmax[1][q], 2);
-      mbar_init(&bars->lsum[q], 2);
-    }
     wc->abort = 0;
     wc->limit_ns = p.wait_ns;
     *sent_count = 0;
@@ -628,13 +655,15 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
     }
   } else {
     // ------------------------------------------------------------ softmax / epilogue (8 warps)
-    // Thread = (row r, key half c): keys [32c, 32c+32) of each page, output
-    // columns [128c, 128c+128) of this CTA's 256.
-    const int quarter = warp & 3;
-    const int c = (warp - kSoftWarp0) >> 2;
-    const int r = quarter * 32 + lane;
+    // A warp has 16 rows, half of its TMEM lane quarter, and two threads per row, lanes
+    // l and l + 16: thread = (row r, key half c), keys [32c, 32c + 32) of each page and output
+    // columns [128c, 128c + 128) of this CTA's 256.  A row's maximum and sum are joined
+    // by one shuffle.
+    const int c = lane >> 4;
+    const int row0 = 32 * (warp & 3) + 16 * ((warp - kSoftWarp0) >> 2);   // the warp's rows
+    const int r = row0 + (lane & 15);
     const int tid = threadIdx.x - kSoftWarp0 * 32;    // 0 .. 255
-    const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+    const uint32_t lane_addr = (uint32_t)row0 << 16;
     const uint32_t x_sendok_peer = mapa(smem_u32(&bars->x_sendok), peer);
     bool out_of_range = false;   // a fp16 partial overflowed: a reference max of +Inf, or a NaN sum
     // The sequence length of the next item is loaded one item ahead, so that
@@ -654,7 +683,7 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
 
       float m_ref = -CUDART_INF_F, l_run = 0.f;
       for (int j = 0; j < n; ++j) {
-        const int gj = g + j, b = gj & 1;
+        const int gj = g + j;
         // full score = fp16(own partial) + fp16(peer partial), identical in both CTAs.
         // The own tile is read (and released) first: it lands before the peer's.
         // P buffer gj & 1 is free once the PV product of page gj - 2 has completed
@@ -717,11 +746,7 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
           const float2 m2 = unpack_f16x2(t[0]);
           mloc = fmaxf(m2.x, m2.y);
         }
-        s_pmax[(b * 2 + c) * kRows + r] = mloc;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->pmax[b][quarter]);
-        if (!warp_wait(&bars->pmax[b][quarter], (gj >> 1) & 1, wc)) goto softmax_fail;
-        const float mx = fmaxf(mloc, s_pmax[(b * 2 + (c ^ 1)) * kRows + r]);
+        const float mx = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 16));
 
         // lazy reference max (log2 domain): move it only when the row max grows by > 2^8
         const float m_new = fmaxf(m_ref, mx);
@@ -753,15 +778,15 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             uint32_t o[32];
-            tmem_ld32(tmem + lane_addr + kTmemO + 128 * c + 32 * q, o);
+            tmem_ld16x2_32<128>(tmem + lane_addr + kTmemO + 32 * q, o);
             tmem_ld_wait();
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-            tmem_st32(tmem + lane_addr + kTmemO + 128 * c + 32 * q, o);
+            tmem_st16x2_32<128>(tmem + lane_addr + kTmemO + 32 * q, o);
           }
           tmem_st_wait();
         }
-        tmem_st16(tmem + lane_addr + kTmemP + 32 * (gj & 1) + 16 * c, pk);   // keys [32c, 32c+32), fp16 pairs
+        tmem_st16x2_16<16>(tmem + lane_addr + kTmemP + 32 * (gj & 1), pk);   // keys [32c, 32c+32), fp16 pairs
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -773,12 +798,10 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
       {
         if (!warp_wait(&bars->o_done, ii & 1, wc)) goto softmax_fail;
         tc_fence_after();
-        float* ls = s_lsum + (ii & 1) * 2 * kRows;    // [item parity][half][row]
-        ls[c * kRows + r] = l_run;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->lsum[quarter]);
-        if (!warp_wait(&bars->lsum[quarter], ii & 1, wc)) goto softmax_fail;
-        l_run = ls[r] + ls[kRows + r];             // same order in both halves
+        {   // the same order in both threads of a row
+          const float other = __shfl_xor_sync(0xffffffffu, l_run, 16);
+          l_run = c == 0 ? l_run + other : other + l_run;
+        }
         out_of_range |= (m_ref == CUDART_INF_F) | (l_run != l_run);
         const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
         const bool valid = r < p.n_heads;
@@ -786,7 +809,7 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           uint32_t o[32];
-          tmem_ld32(tmem + lane_addr + kTmemO + 128 * c + 32 * q, o);
+          tmem_ld16x2_32<128>(tmem + lane_addr + kTmemO + 32 * q, o);
           tmem_ld_wait();
           if (!valid) continue;
           const int col = 256 * rank + 128 * c + 32 * q;
