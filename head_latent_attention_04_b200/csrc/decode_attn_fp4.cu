@@ -14,13 +14,14 @@
 // P . c_KV), so no product can run on the 4-bit codes: every half page is
 // widened to fp16 in shared memory.  No unit is saturated (tensor pipe 29 %, issue
 // slots 34 %, shared memory 40 % on 32 x 4096 tokens): the kernel is bound by the
-// serial chains of its warps.  The sender warps' turn per 64-key page (widen 880 cycles,
-// four waits of 200 to 450, conversion and store of the scores 450) and the softmax warps' (2400) set the pace, about
-// 2450 cycles, of which the tensor pipe needs 1088.  4 x 128K tokens: 148 us launched from a graph,
-// 173 us launched back to back for a second, where the card's power limit holds the SM
-// clock at 1.69 of 1.965 GHz; in that loop the bf16 cache's kernel takes 183 us, the FP8
-// cache's 188 (32 x 4096 tokens: 50 against 55 and 58).  So the 4-bit cache holds
-// 2.8 times the tokens of bf16 and is a little faster.
+// serial chains of its warps, and three of them turn once per 64-key page in about 2400 cycles
+// each, of which the tensor pipe needs 1088: the sender warps (two stages' waits,
+// widening 570, the scores' wait, conversion and store 700), the softmax warps (2500), and the exchange (a copy
+// takes 1050, the answer that the tile is free and the next copy's start as long again).
+// 4 x 128K tokens: 142 us launched from a graph, 167 us launched back to back for a second, where the
+// card's power limit holds the SM clock at 1.6 of 1.965 GHz; in that loop the bf16
+// cache's kernel takes 183 us, the FP8 cache's 188 (32 x 4096 tokens: 49 against 55
+// and 58).  So the 4-bit cache holds 2.8 times the tokens of bf16 and is a little faster.
 //
 // Why this shape (as in decode_attn.cu).  O for 128 heads x 512 columns in fp32 is
 // one SM's whole tensor memory, so a cluster of two CTAs splits the latent
@@ -41,20 +42,20 @@
 // it), two P buffers [320, 352) and [352, 384) in fp16 (page g uses buffer g & 1),
 // q_lat half [384, 512) in fp16 pairs.
 //
-// Warps (512 threads): 0 TMA; 1 QK issuer, owner of the tensor memory; 2 PV issuer;
-// 3-6 query loader, widening and score sender (one thread per row); 7-14 softmax, correction, epilogue
-// (two warps per TMEM lane quarter, one per 32-key half); 15 copies score tiles to the peer.
-// Steps (4 x 128K tokens, from a graph): the widening in the sender warps with a ring of
-// its own for the raw pages 160 us; 16 loads of a row's query in flight 157; the wait for
-// the own tile before, not after, the scores are read 149 (it is over by then, and the
-// scores' registers are not live across it); the wait for a P buffer at the start
-// of a page 148.  Measured and not kept: four more warps for the widening alone 167 to 181 us (each SM
-// sub-partition then runs five warps whose chains slow one another down, and the softmax
-// warps set the pace); two softmax groups taking pages in turn with one thread per row
-// 198; two tiles for the peer's scores, no change; one wait for two barriers at
-// once 181 to 262; one lane waiting for its warp 480; test_wait before try_wait 157; codes widened by
-// byte permutes instead of the conversion instruction 203; queries read past L1
-// 6 us more per work item.
+// Warps (640 threads): 0 TMA; 1 QK issuer, owner of the tensor memory; 2 PV issuer;
+// 3-6 and 16-19 query loader, widening and score sender; 7-14 softmax, correction, epilogue
+// (16 rows each, two threads per row); 15 copies score tiles to the peer.
+// Steps (4 x 128K tokens, from a graph): four sender warps with a ring of its own for
+// the raw pages 160 us; a query's loads 16 at a time 157; the scores read
+// when the own tile is free, their registers not live across that wait, 149; the wait for a P
+// buffer at the start of a page 148; a row's two softmax threads in one warp, joined by
+// a shuffle instead of a barrier, 145; eight sender warps 143.5, which read and free S before they wait
+// for the own tile 142.  Measured and not kept: a group of warps for the
+// widening alone 144 to 181 us; two softmax groups taking pages in turn with one thread
+// per row 198; two tiles for the peer's scores (and three raw stages) 145; two or three barriers polled at once
+// 141.5 to 144; one wait for two barriers by different lanes 181 to 262; one lane waiting for its warp
+// 480; test_wait before try_wait 157; widening two pages ahead 174; codes widened by byte permutes instead of the
+// conversion instruction 203.
 //
 // Failure: every wait is bounded (200 ms by default, mla_set_wait_limit_ns); a role that
 // gives up sets MLA_STATUS_TIMEOUT, stops its peer, drains the copies and products it
@@ -97,9 +98,9 @@ constexpr int kOffXOwn = kOffXPeer + kXBytes;                // own partial scor
 constexpr int kOffQRope = kOffXOwn + kXBytes;                // bf16 q_rope half, 128 rows x 64 B (SW64, A of QK)
 constexpr int kOffBar = kOffQRope + kRows * 64;
 
-constexpr int kThreads = 512;            // 16 warps
-constexpr int kSoftWarp0 = 7, kCopyWarp = 15;   // senders are warps 3 .. 6
-constexpr int kSoftWarps = 8;
+constexpr int kThreads = 640;            // 20 warps
+constexpr int kSoftWarp0 = 7, kCopyWarp = 15, kSendWarp1 = 16;   // senders are warps 3 .. 6 and 16 .. 19
+constexpr int kSoftWarps = 8, kSendWarps = 8;
 
 constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemP = 320, kTmemQ = 384, kTmemCols = 512;   // P: two 32-column buffers
 constexpr float kLn2 = 0.6931471805599453f;
@@ -124,12 +125,12 @@ struct DecodeParams {
 struct Bars {
   uint64_t raw_full[kRawStages];    // the TMA has landed
   uint64_t raw_empty[kRawStages];   // its QK product is complete (it was widened before that)
-  uint64_t kv_conv[kStages];        // widened to fp16 (4 sender warps)
+  uint64_t kv_conv[kStages];        // widened to fp16 (8 sender warps)
   uint64_t kv_empty[kStages];       // its PV product is complete
   uint64_t q_full, q_empty;
   uint64_t s_full;       // QK product of the current page is in S
   uint64_t s_read;       // the sender has read S (the next QK may overwrite it)
-  uint64_t own_full;     // own fp16 partial-score tile written (4 sender warps)
+  uint64_t own_full;     // own fp16 partial-score tile written (8 sender warps)
   uint64_t own_free;     // own tile read by the softmax (8 warps) and by its bulk copy (1)
   uint64_t x_recv;       // peer's fp16 partial scores landed in the peer tile (1 arrival + 16 KB tx)
   uint64_t x_sendok;     // peer has read its peer tile, which this CTA may refill (8 remote arrivals)
@@ -277,14 +278,14 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
       mbar_init(&bars->raw_empty[s], 1);
     }
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bars->kv_conv[s], 4);
+      mbar_init(&bars->kv_conv[s], kSendWarps);
       mbar_init(&bars->kv_empty[s], 1);
     }
-    mbar_init(&bars->q_full, 4);       // the 4 q_lat / q_rope loader warps
+    mbar_init(&bars->q_full, kSendWarps);
     mbar_init(&bars->q_empty, 1);
     mbar_init(&bars->s_full, 1);
-    mbar_init(&bars->s_read, 4);
-    mbar_init(&bars->own_full, 4);
+    mbar_init(&bars->s_read, kSendWarps);
+    mbar_init(&bars->own_full, kSendWarps);
     mbar_init(&bars->own_free, kSoftWarps + 1);
     mbar_init(&bars->x_recv, 1);
     mbar_init(&bars->x_sendok, kSoftWarps);
@@ -478,22 +479,24 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
     __syncwarp();
     mma_commit_elect(&bars->pv_done);
     mbar_drain(&bars->pv_done, 0);
-  } else if (warp < kSoftWarp0) {
-    // ------------------------------------------------------------ query loader and score sender (4 warps)
-    // At each item start the thread of row r copies its 256 q_lat columns and
-    // its 32 q_rope columns into TMEM (A operands of the QK product) once the
+  } else if (warp < kSoftWarp0 || warp >= kSendWarp1) {
+    // ------------------------------------------------------------ query loader, widening, score sender (8 warps)
+    // Two warps per TMEM lane quarter, thread = (row r, half).  At each item start
+    // it copies half of row r's 256 q_lat columns into TMEM and (half 0) its 32
+    // q_rope columns into shared memory (A operands of the QK product) once the
     // previous item's last QK has completed; the producer has prefetched those
-    // rows into L2.  Per page it reads this CTA's partial scores (its 288
-    // columns) as soon as the QK product lands, frees S, rounds to fp16 into
+    // rows into L2.  Per page it reads 32 keys of this CTA's partial scores
+    // as soon as the QK product lands, frees S, rounds to fp16 into
     // the own tile, and the copy warp pushes that tile to the peer's tile with a
-    // bulk copy that completes on the peer's x_recv.  Thread = one row, 64
-    // keys; 16-byte chunks XOR-swizzled by (row & 7).
+    // bulk copy that completes on the peer's x_recv (16-byte chunks XOR-swizzled
+    // by row & 7).
     const int quarter = warp & 3;
+    const int half = warp >= kSendWarp1 ? 1 : 0;
     const int r = quarter * 32 + lane;
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
     const float sl2 = p.scale_log2;
-    // Widens page gg to fp16.  Thread = (key cr, 128 of this CTA's 256 columns):
-    // 64 bytes of codes, four groups of 32 columns, each 16 bytes with one scale;
+    // Widens page gg to fp16.  Thread = (key cr, 64 of this CTA's 256 columns):
+    // 32 bytes of codes, two groups of 32 columns, each 16 bytes with one scale;
     // a group's codes become fp16 by the conversion instruction, exactly, and are
     // multiplied by the scale, one rounding.  Page g + 1 is widened before page
     // g's scores are awaited (pages 0 and 1 before page 0's), that is, right after
@@ -504,32 +507,28 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
       if (!warp_wait(&bars->raw_full[sr], (gg / kRawStages) & 1, wc) ||
           (gg >= kStages && !warp_wait(&bars->kv_empty[s], ((gg / kStages) - 1) & 1, wc)))
         return false;
-      const int ch = lane >> 4;
+      const int ch = lane >> 3;
       // (recomputed per call: kept live across the sender loop they cost registers)
       int cr;
-      asm volatile("mov.b32 %0, %1;" : "=r"(cr) : "r"(16 * (warp - 3) + (lane & 15)));
+      asm volatile("mov.b32 %0, %1;" : "=r"(cr) : "r"(8 * (4 * half + (warp - 3) % 13) + (lane & 7)));
       const uint32_t raw = smem_u32(s_raw + sr * kRawBytes);
       const uint32_t codes = raw + kRawCodes + cr * 128;
-      uint32_t s01, s23;   // the scales of the four groups
-      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                   : "=r"(s01), "=r"(s23)
-                   : "r"(raw + kRawScales + cr * 16 + ch * 8)
-                   : "memory");
-      const uint32_t row = smem_u32(s_kv + s * kStageBytes) + 2 * ch * kChunkBytes + cr * 128;
-      uint4 raw_codes[4];   // (all reads before the first write: their latencies overlap)
+      uint32_t s01;   // the scales of the two groups
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(s01) : "r"(raw + kRawScales + cr * 16 + ch * 4) : "memory");
+      const uint32_t row = smem_u32(s_kv + s * kStageBytes) + ch * kChunkBytes + cr * 128;
+      uint4 raw_codes[2];   // (all reads before the first write: their latencies overlap)
 #pragma unroll
-      for (int gi = 0; gi < 4; ++gi) raw_codes[gi] = ld_shared_v4(codes + (((4 * ch + gi) ^ (cr & 7)) << 4));
+      for (int gi = 0; gi < 2; ++gi) raw_codes[gi] = ld_shared_v4(codes + (((2 * ch + gi) ^ (cr & 7)) << 4));
 #pragma unroll
-      for (int gi = 0; gi < 4; ++gi) {
+      for (int gi = 0; gi < 2; ++gi) {
         const uint4 v = raw_codes[gi];
-        const uint32_t sc2 = __byte_perm(gi < 2 ? s01 : s23, 0, (gi & 1) ? 0x3232 : 0x1010);
+        const uint32_t sc2 = __byte_perm(s01, 0, gi ? 0x3232 : 0x1010);
         const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
-        const uint32_t dst = row + (gi >> 1) * kChunkBytes;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {   // 8 codes -> one 16-byte chunk
           uint32_t o[4];
           dequant_e2m1x8_f16(wd[k], sc2, o);
-          st_shared_v4(dst + (((4 * (gi & 1) + k) ^ (cr & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+          st_shared_v4(row + (((4 * gi + k) ^ (cr & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
         }
       }
       fence_proxy_async_smem();   // read by the tensor cores
@@ -546,7 +545,7 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
       const int ii = it - it_begin;
       if (ii > 0 && !warp_wait(&bars->q_empty, (ii - 1) & 1, wc)) goto sender_fail;
       {
-        {
+        if (half == 0) {
           const uint4* rsrc = reinterpret_cast<const uint4*>(p.q_rope + ((size_t)w[kItRow] * p.n_heads + r) * 64 +
                                                              32 * rank);
           // row r of the K-major A tile, 64 bytes: 16-byte chunk k at (k ^ ((r >> 1) & 3))
@@ -561,21 +560,20 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
         }
         const uint4* src = reinterpret_cast<const uint4*>(p.q_lat + ((size_t)w[kItRow] * p.n_heads + r) * 512 +
                                                           256 * rank);
-        // the latent products take fp16 operands.  128 columns at a time: 16 loads in flight
-        // (plain loads: the eight pieces of a line that a row's thread reads one after
-        // the other come from L1; through L2 alone an item started 6 us later)
+        // the latent products take fp16 operands (plain loads: the eight pieces of a
+        // line that a row's thread reads one after the other come from L1; through
+        // L2 alone an item started 6 us later)
 #pragma unroll 1
-        for (int hh = 0; hh < 2; ++hh) {
-          uint32_t v[64];
+        for (int hh = 2 * half; hh < 2 * half + 2; ++hh) {
+          uint32_t v[32];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const uint4 q = r < p.n_heads ? src[16 * hh + k] : make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < 8; ++k) {
+            const uint4 q = r < p.n_heads ? src[8 * hh + k] : make_uint4(0, 0, 0, 0);
             v[4 * k] = q.x; v[4 * k + 1] = q.y; v[4 * k + 2] = q.z; v[4 * k + 3] = q.w;
           }
 #pragma unroll
-          for (int k = 0; k < 64; ++k) v[k] = bf16x2_to_f16x2(v[k]);
-          tmem_st32(tmem + lane_addr + kTmemQ + 64 * hh, *reinterpret_cast<uint32_t(*)[32]>(v));
-          tmem_st32(tmem + lane_addr + kTmemQ + 64 * hh + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+          for (int k = 0; k < 32; ++k) v[k] = bf16x2_to_f16x2(v[k]);
+          tmem_st32(tmem + lane_addr + kTmemQ + 32 * hh, v);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -587,26 +585,25 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
         // pages up to g + 1: at g = 0 pages 0 and 1, then one per page
         for (; widened < min(g + 2, pages_total); ++widened)
           if (!widen(widened)) goto sender_fail;
-        uint32_t v[64];
-        // single tile: page g - 1's own tile must have been read by the softmax and the copy
-        if (g >= 1 && !warp_wait(&bars->own_free, (g - 1) & 1, wc)) goto sender_fail;
+        uint32_t v[32];
         if (!warp_wait(&bars->s_full, g & 1, wc)) goto sender_fail;
         tc_fence_after();
-        tmem_ld32(tmem + lane_addr + kTmemS, *reinterpret_cast<uint32_t(*)[32]>(v));
-        tmem_ld32(tmem + lane_addr + kTmemS + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+        tmem_ld32(tmem + lane_addr + kTmemS + 32 * half, v);
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->s_read);
-        uint32_t hv[32];
+        uint32_t hv[16];
 #pragma unroll
-        for (int k = 0; k < 32; ++k)   // scaled to log2 units, then rounded to fp16
+        for (int k = 0; k < 16; ++k)   // scaled to log2 units, then rounded to fp16
           hv[k] = pack_f16(__uint_as_float(v[2 * k]) * sl2, __uint_as_float(v[2 * k + 1]) * sl2);
+        // single tile: page g - 1's own tile must have been read by the softmax and the copy
+        if (g >= 1 && !warp_wait(&bars->own_free, (g - 1) & 1, wc)) goto sender_fail;
         {
           uint8_t* own = s_xown + r * kXRow;
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(own + ((k ^ (r & 7)) << 4)) =
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(own + (((4 * half + k) ^ (r & 7)) << 4)) =
                 make_uint4(hv[4 * k], hv[4 * k + 1], hv[4 * k + 2], hv[4 * k + 3]);
         }
         fence_proxy_async_smem();   // the copy warp's bulk copy reads the tile through the async proxy
@@ -622,7 +619,7 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
   } else if (warp == kCopyWarp) {
     // ------------------------------------------------------------ score copy (one thread)
     // Per page: one bulk copy of the own fp16 tile to the peer's tile,
-    // completing on the peer's x_recv, once the 4 sender warps have written
+    // completing on the peer's x_recv, once the 8 sender warps have written
     // it and the peer has read page g - 1 out of its tile.  The own tile may
     // be rewritten once the copy has read it (own_free).  A warp of its own,
     // so that waiting for the copy never holds back the next page's score read.
@@ -636,8 +633,8 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
         const int32_t* w = items + (size_t)it * kItemWords;
         const int n = w[kItPageEnd] - w[kItPageBegin];
         for (int j = 0; j < n; ++j, ++g) {
-          if (!mbar_wait<false, kWaitHintNs>(&bars->own_full, g & 1, wc) ||
-              (g >= 1 && !mbar_wait<false, kWaitHintNs>(&bars->x_sendok, (g - 1) & 1, wc))) {
+          if ((g >= 1 && !mbar_wait<false, kWaitHintNs>(&bars->x_sendok, (g - 1) & 1, wc)) ||
+              !mbar_wait<false, kWaitHintNs>(&bars->own_full, g & 1, wc)) {
             ok = false;
             break;
           }
