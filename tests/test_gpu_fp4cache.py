@@ -132,6 +132,35 @@ def test_padding_is_skipped_and_bad_slots_are_reported(mla):
     assert status.item() == mla.STATUS_BAD_BLOCK and torch.all(out == 3.0)
 
 
+@pytest.mark.parametrize("n", [4097, 8288, 8289, 16301])
+def test_long_calls_are_exact_too(mla, n):
+    """Both forms of the row kernels, one and four rows a thread: padding, bad slots and a ragged end."""
+    nb = 300
+    kv = rows_of_many_ranges(n, n)
+    rng = np.random.default_rng(n)
+    s = rng.permutation(nb * 64)[:n].astype(np.int32)
+    s[rng.permutation(n)[:97]] = -1
+    s[[0, n - 1]] = -1
+    live = s >= 0
+    pool = torch.full((nb, 64, ROW4), 0xAB, dtype=torch.uint8, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    slots = torch.from_numpy(s).to(DEV)
+    mla.kv_quantize_fp4(kv.to(DEV), slots, pool, status)
+    back = torch.full((n, 576), 3.0, dtype=torch.bfloat16, device=DEV)
+    mla.kv_dequantize_fp4(pool, slots, back, status)
+    assert status.item() == 0
+    got, want = pool.reshape(-1, ROW4).cpu().numpy(), pack_rows(kv)
+    assert np.array_equal(got[s[live], 256:], want[live, 256:])
+    assert np.array_equal(F.e2m1_values(F.unpack(got[s[live]])[0]), F.e2m1_values(F.unpack(want[live])[0]))
+    assert np.all(np.delete(got, s[live], axis=0) == 0xAB)
+    exact = torch.from_numpy(F.dequantize_rows(want)).to(torch.bfloat16)
+    exact[~torch.from_numpy(live)] = 3.0
+    assert torch.equal(back.cpu(), exact)
+    slots[n // 2] = nb * 64
+    mla.kv_quantize_fp4(kv.to(DEV), slots, pool, status)
+    assert status.item() == mla.STATUS_BAD_BLOCK
+
+
 @pytest.mark.parametrize("value", [65536.0, 1e30, float("inf"), float("nan"), float("-inf")])
 def test_values_beyond_fp16_are_flagged_and_stay_finite(mla, value):
     kv = rows_of_many_ranges(4, 2)

@@ -86,6 +86,12 @@ def test_wide_slot_maps_leave_the_same_answers(mla, max_new):
     check_tables(mla, [70] * 30, [1333] * 30, 40, 400, max_new=max_new)
 
 
+@pytest.mark.parametrize("max_new", [7167, 7168, 7169, 8193])
+def test_slot_maps_around_the_second_launch(mla, max_new):
+    check_tables(mla, [70] * 30, [233] * 30, 40, 400, max_new=max_new)             # 6990 tokens
+    check_tables(mla, [63, 0, 128], [max_new - 5, 0, 5], 140, 300, max_new=max_new)   # full to the last slot
+
+
 def test_bad_blocks_are_reported(mla):
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
     table = i32([[3, 99, -1], [-4, -1, -1]])
