@@ -12,16 +12,16 @@
 // rate: the floor is the tensor cores' (4 x 128K tokens: 89 us).  The scales vary
 // along both products' reduction or output axes (a key's groups along q_lat . c_KV, keys along
 // P . c_KV), so no product can run on the 4-bit codes: every half page is
-// widened to fp16 in shared memory.  No unit is saturated (tensor pipe 29 %, issue
-// slots 34 %, shared memory 40 % on 32 x 4096 tokens): the kernel is bound by the
+// widened to fp16 in shared memory.  No unit is saturated (tensor pipe 34 %, issue
+// slots 47 %, shared memory 46 % on 32 x 4096 tokens): the kernel is bound by the
 // serial chains of its warps, and three of them turn once per 64-key page in about 2400 cycles
 // each, of which the tensor pipe needs 1088: the sender warps (two stages' waits,
 // widening 570, the scores' wait, conversion and store 700), the softmax warps (2500), and the exchange (a copy
 // takes 1050, the answer that the tile is free and the next copy's start as long again).
-// 4 x 128K tokens: 142 us launched from a graph, 167 us launched back to back for a second, where the
+// 4 x 128K tokens: 142 us launched from a graph, 165 us launched back to back for a second, where the
 // card's power limit holds the SM clock at 1.6 of 1.965 GHz; in that loop the bf16
-// cache's kernel takes 183 us, the FP8 cache's 188 (32 x 4096 tokens: 49 against 55
-// and 58).  So the 4-bit cache holds 2.8 times the tokens of bf16 and is a little faster.
+// cache's kernel takes 178 us, the FP8 cache's 186 (32 x 4096 tokens: 49 against 54
+// and 57).  So the 4-bit cache holds 2.8 times the tokens of bf16 and is a little faster.
 //
 // Why this shape (as in decode_attn.cu).  O for 128 heads x 512 columns in fp32 is
 // one SM's whole tensor memory, so a cluster of two CTAs splits the latent

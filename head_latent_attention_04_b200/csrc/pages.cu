@@ -206,9 +206,11 @@ summarize_pages_kernel(const uint8_t* pool, const int32_t* blocks, int num_block
 // 16-byte asynchronous copies (A, K-major; two buffers, and two in tensor
 // memory), so that a tile's product and the next tile's copies run under the
 // maxima of the tile before.  At one tile a block (4 rows of 2048 pages on 148
-// SMs) it is all latency: 6.9 us, of which 2.2 are two dependent reads and the
-// quantisation of 147 KB of queries; where a block walks its row a tile costs
-// 0.9 us.  The grid cuts a row into as many runs as fill the card.
+// SMs) it is all latency: 7.9 us, of which 2.5 are dependent reads and the issue of the
+// copies, 3.4 the quantisation of 147 KB of queries, 1.1 the wait for the copies
+// and the product, 0.9 the maxima; where a block walks its row a further tile costs
+// 2.1 us, mostly waiting for its 74 KB.  With the selection behind it: 14.8 us for
+// 4 rows of 2048 pages, 28.2 for 122 rows of up to 1024.  The grid cuts a row into as many runs as fill the card.
 constexpr int kScoreThreads = 512;
 constexpr int kTile = 128;
 constexpr int kChunkBytes = kTile * 128;          // 128 rows x 128 K-bytes (SW128)
