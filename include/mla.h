@@ -294,7 +294,7 @@ mla_status_t mla_kv_quantize_fp8(const void* kv, const int32_t* slots, int64_t n
  * columns with one fp16 scale each, in E2M1 codes (the values 0, .5, 1, 1.5, 2,
  * 3, 4, 6 and their negatives are codes 0..7 and 8..15).  Token row:
  *   bytes [0, 256)    codes, column 2i in the low nibble of byte i, 2i + 1 in the high one
- *   bytes [256, 288)  fp16 scales s_0..s_15, c_KV[t, c] = code[c] * s_{c / 32}
+ *   bytes [256, 288)  fp16 scales s_0..s_15 >= 0, c_KV[t, c] = code[c] * s_{c / 32}
  *   bytes [288, 416)  k_rope[t, 0..63] in bf16 (not quantised)
  *   kv_pool_fp4  uint8 [num_blocks][64][416], 16-byte aligned (mla_kv_quantize_fp4 writes it)
  * Numerics: rows are widened on chip to fp16 (code * scale, rounded once), q_lat is rounded to
@@ -389,7 +389,8 @@ mla_status_t mla_plan_device(const mla_dims_t* dims, const int32_t* seq_lens, in
  * page's 64 rows [c_KV | k_rope], scale = amax / 127, code = rint(127 m / amax)
  * (0 and 0 when amax = 0).  Call it when a page fills; a page that still grows needs none (it
  * is among the recent pages).
- *   kv_pool   the pool, of kind `cache` (MLA_CACHE_BF16, _FP8 or _FP4)
+ *   kv_pool   the pool, of kind `cache` (MLA_CACHE_BF16, _FP8 or _FP4); the pages' values must be
+ *             finite (a summary of others holds no meaning, and is not reported)
  *   blocks    int32 [n]  pages to summarise; -1 is skipped, others outside the pool are reported
  *             (MLA_STATUS_BAD_BLOCK) and skipped
  *   codes     int8 [num_blocks][576], 16-byte aligned, and scales fp32 [num_blocks]: the entries of
