@@ -134,7 +134,10 @@ struct Bars {
   uint64_t own_free;     // own tile read by the softmax (8 warps) and by its bulk copy (1)
   uint64_t x_recv;       // peer's fp16 partial scores landed in the peer tile (1 arrival + 16 KB tx)
   uint64_t x_sendok;     // peer has read its peer tile, which this CTA may refill (8 remote arrivals)
-  uint64_t p_full;       // P written (O rescaled if needed), 8 softmax warps
+  // P written (O rescaled if needed), 8 softmax warps.  One per P buffer, as o_full: the softmax writes
+  // page g + 2's P only after page g's product, so no phase passes before the PV issuer has seen
+  // it (with one barrier for both, pages g and g + 1 could).
+  uint64_t p_full[2];
   uint64_t o_full[2];     // PV product of a page complete, per P buffer (page g uses buffer g & 1)
   uint64_t o_done;        // every PV product of the current item complete (epilogue)
   uint64_t o_free, qk_done, pv_done;
@@ -289,7 +292,8 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
     mbar_init(&bars->own_free, kSoftWarps + 1);
     mbar_init(&bars->x_recv, 1);
     mbar_init(&bars->x_sendok, kSoftWarps);
-    mbar_init(&bars->p_full, kSoftWarps);
+    mbar_init(&bars->p_full[0], kSoftWarps);
+    mbar_init(&bars->p_full[1], kSoftWarps);
     mbar_arrive_expect_tx(&bars->x_recv, kXBytes);   // armed for page 0
     mbar_init(&bars->o_full[0], 1);
     mbar_init(&bars->o_full[1], 1);
@@ -454,7 +458,7 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
       const int ii = it - it_begin;
       for (int j = 0; j < n; ++j, ++g) {
         const int s = g % kStages;
-        if (!warp_wait(&bars->p_full, g & 1, wc) ||
+        if (!warp_wait(&bars->p_full[g & 1], (g >> 1) & 1, wc) ||
             (j == 0 && ii > 0 && !warp_wait(&bars->o_free, (ii - 1) & 1, wc))) {
           ok = false;
           break;
@@ -787,7 +791,7 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full);
+        if (lane == 0) mbar_arrive(&bars->p_full[gj & 1]);
       }
 
       // epilogue: O / l  ->  o_lat (whole row) or the row's partial slot.  A
