@@ -117,6 +117,7 @@ struct DecodeParams {
   int n_heads, max_blocks, num_blocks, s_q, causal, B, n_rows, num_clusters;
   float scale_log2;             // scale * log2(e)
   uint64_t wait_ns;             // limit of every protocol wait (drains of issued work use the default)
+  uint32_t zero;                // 0, read at run time (see the release of the peer tile)
 };
 
 struct Bars {
@@ -627,7 +628,7 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_consta
         const int n = w[kItPageEnd] - w[kItPageBegin];
         for (int j = 0; j < n; ++j, ++g) {
           if (!mbar_wait<false, kWaitHintNs>(&bars->own_full, g & 1, wc) ||
-              (g >= 1 && !mbar_wait<false, kWaitHintNs>(&bars->x_sendok, (g - 1) & 1, wc))) {
+              (g >= 1 && !mbar_wait<true, kWaitHintNs>(&bars->x_sendok, (g - 1) & 1, wc))) {
             ok = false;
             break;
           }
@@ -708,10 +709,14 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_consta
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             pr[k] = *reinterpret_cast<const uint4*>(xrow + (((off_base + k) ^ (r & 7)) << 4));
-          // the peer tile is consumed: re-arm x_recv for page gj + 1, then let the peer refill it
-          uint32_t ok_addr = x_sendok_peer;
-          asm volatile("" : "+r"(ok_addr) : "r"(pr[0].x ^ pr[1].x ^ pr[2].x ^ pr[3].x));
-          __syncwarp();
+          // The peer tile is consumed: re-arm x_recv for page gj + 1, then let the peer refill it.
+          // Its next copy must come after every lane's reads.  A release at cluster scope would say
+          // so, but it waits for all that the CTA has in flight (4 x 128K tokens: 151 -> 209 us); the
+          // arrive instead depends on what was read: its address takes in a vote over all four loads
+          // of every lane (p.zero is 0, which the compiler does not know), so it cannot be
+          // issued before they have returned.
+          const uint32_t read = (pr[0].x ^ pr[1].x ^ pr[2].x ^ pr[3].x) & p.zero;
+          const uint32_t ok_addr = x_sendok_peer + __ballot_sync(0xffffffffu, read != 0);
           if (lane == 0) {
             if (warp == kSoftWarp0) mbar_arrive_expect_tx(&bars->x_recv, kXBytes);
             mbar_arrive_relaxed_cluster(ok_addr);
@@ -979,6 +984,7 @@ mla_status_t launch_decode_impl(const mla_dims_t& d, const void* q_lat, const vo
   p.num_clusters = num_clusters;
   p.scale_log2 = d.scale * 1.4426950408889634f;
   p.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  p.zero = 0;
 
   cudaError_t e = decode_smem_attr<kFp8, kTree>();
   if (e == cudaSuccess) {

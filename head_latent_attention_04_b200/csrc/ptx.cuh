@@ -46,7 +46,7 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
 }
 
 // Relaxed arrive on a barrier given by its shared::cluster address: a signal
-// with no memory ordering (the caller orders its own accesses beforehand).
+// with no memory ordering of its own.
 __device__ __forceinline__ void mbar_arrive_relaxed_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");

@@ -188,3 +188,16 @@ def test_the_model_sees_a_lapped_barrier():
     product's issuer looks, whose wait then never ends."""
     assert not finishes(4, True, 1, last(0, "pv"))
     assert finishes(4, True, 2, last(0, "pv"))
+
+
+@pytest.mark.parametrize("kernel", ["decode_attn", "decode_attn_fp4"])
+def test_the_peer_tile_is_read_before_it_is_refilled(kernel):
+    """The arrive that lets the peer copy into this CTA's tile depends on what every lane read there
+    (an empty asm statement is no instruction and orders nothing), and the thread that copies
+    acquires it at cluster scope."""
+    text = " ".join(re.sub(r"//.*", "", source(kernel)).split())
+    assert "const uint32_t read = (pr[0].x ^ pr[1].x ^ pr[2].x ^ pr[3].x) & p.zero; " \
+           "const uint32_t ok_addr = x_sendok_peer + __ballot_sync(0xffffffffu, read != 0);" in text
+    assert text.count("mbar_arrive_relaxed_cluster(") == text.count("mbar_arrive_relaxed_cluster(ok_addr)") == 1
+    assert text.count("mbar_wait<true, kWaitHintNs>(&bars->x_sendok") == 1
+    assert "mbar_wait<false, kWaitHintNs>(&bars->x_sendok" not in text
