@@ -224,6 +224,14 @@ mla_status_t mla_plan(const mla_dims_t* dims, const int32_t* seq_lens_host, int3
                     (int64_t)(plan_bytes / 4), num_slots);
 }
 
+// Workspaces given without their sizes: those of mla_plan_size, which no plan of these dims exceeds;
+// none when either is NULL (a plan that splits a row is then refused on the device).
+static PlanRoom plan_room(const mla_dims_t& d, int32_t num_clusters, const float* o_part, const float* lse_part) {
+  const int32_t n = d.B * d.s_q;
+  return {(int)plan_words_upper_bound(num_clusters, n),
+          o_part && lse_part ? (int)plan_slots_upper_bound(num_clusters, n) : 0};
+}
+
 mla_status_t mla_decode_attn(const mla_dims_t* dims, const void* q_lat, const void* q_rope,
                              const void* kv_pool, const int32_t* block_table,
                              const int32_t* seq_lens, const void* plan_dev, int32_t num_clusters,
@@ -240,12 +248,11 @@ mla_status_t mla_decode_attn(const mla_dims_t* dims, const void* q_lat, const vo
   MLA_TRY(check_ptr(o_lat, "o_lat"));
   if (num_clusters < 1 || num_clusters > 4096)
     return set_error(MLA_ERR_INVALID_ARG, "num_clusters must be in [1, 4096]");
-  // o_part / lse_part may be NULL only when the plan splits no row; the kernel
-  // checks slots against the plan, the host cannot see the device plan here.
   if ((o_part && (reinterpret_cast<uintptr_t>(o_part) & 31u)) || (lse_part && (reinterpret_cast<uintptr_t>(lse_part) & 3u)))
     return set_error(MLA_ERR_INVALID_ARG, "o_part must be 32-byte aligned, lse_part 4-byte aligned");
   return launch_decode_attn(*dims, q_lat, q_rope, kv_pool, block_table, seq_lens, nullptr,
                             static_cast<const int32_t*>(plan_dev), num_clusters, o_part, lse_part,
+                            plan_room(*dims, num_clusters, o_part, lse_part),
                             o_lat, lse_out, status, stream);
 }
 
@@ -272,6 +279,7 @@ mla_status_t mla_decode_attn_tree(const mla_dims_t* dims, const void* q_lat, con
     return set_error(MLA_ERR_INVALID_ARG, "o_part must be 32-byte aligned, lse_part 4-byte aligned");
   return launch_decode_attn(*dims, q_lat, q_rope, kv_pool, block_table, seq_lens, draft_masks,
                             static_cast<const int32_t*>(plan_dev), num_clusters, o_part, lse_part,
+                            plan_room(*dims, num_clusters, o_part, lse_part),
                             o_lat, lse_out, status, stream);
 }
 
@@ -295,6 +303,7 @@ mla_status_t mla_decode_attn_fp8cache(const mla_dims_t* dims, const void* q_lat,
     return set_error(MLA_ERR_INVALID_ARG, "o_part must be 32-byte aligned, lse_part 4-byte aligned");
   return launch_decode_attn_fp8cache(*dims, q_lat, q_rope, kv_pool_fp8, block_table, seq_lens,
                                      static_cast<const int32_t*>(plan_dev), num_clusters, o_part, lse_part,
+                            plan_room(*dims, num_clusters, o_part, lse_part),
                                      o_lat, lse_out, status, stream);
 }
 
@@ -370,6 +379,7 @@ mla_status_t mla_decode_attn_fp4cache(const mla_dims_t* dims, const void* q_lat,
     return set_error(MLA_ERR_INVALID_ARG, "o_part must be 32-byte aligned, lse_part 4-byte aligned");
   return launch_decode_attn_fp4cache(*dims, q_lat, q_rope, kv_pool_fp4, block_table, seq_lens,
                                      static_cast<const int32_t*>(plan_dev), num_clusters, o_part, lse_part,
+                            plan_room(*dims, num_clusters, o_part, lse_part),
                                      o_lat, lse_out, status, stream);
 }
 
@@ -472,8 +482,76 @@ mla_status_t mla_combine(const mla_dims_t* dims, const void* plan_dev, const flo
   MLA_TRY(check_ptr(plan_dev, "plan_dev"));
   MLA_TRY(check_ptr(o_lat, "o_lat"));
   if (!o_part || !lse_part) return set_error(MLA_ERR_INVALID_ARG, "o_part / lse_part is NULL");
+  // (the cluster count is not an argument: the largest plan there can be)
   return launch_combine(*dims, static_cast<const int32_t*>(plan_dev), dims->B * dims->s_q, o_part,
-                        lse_part, o_lat, lse_out, stream);
+                        lse_part, plan_room(*dims, 4096, o_part, lse_part), o_lat, lse_out, nullptr, stream);
+}
+
+// Pointers and workspaces of the two entry points that are given the buffers' sizes.
+static mla_status_t check_sized(const mla_dims_t& d, const void* plan_dev, size_t plan_bytes, int32_t num_clusters,
+                                const float* o_part, const float* lse_part, int32_t part_slots, PlanRoom* room) {
+  MLA_TRY(check_words(plan_dev, "plan_dev"));
+  if (part_slots < 0) return set_error(MLA_ERR_INVALID_ARG, "part_slots must be >= 0");
+  if (part_slots > 0) {
+    if (!o_part || !lse_part) return set_error(MLA_ERR_INVALID_ARG, "part_slots > 0 needs o_part and lse_part");
+    if ((reinterpret_cast<uintptr_t>(o_part) & 31u) || (reinterpret_cast<uintptr_t>(lse_part) & 3u))
+      return set_error(MLA_ERR_INVALID_ARG, "o_part must be 32-byte aligned, lse_part 4-byte aligned");
+  }
+  // header, cluster ranges and row section: what is read before the plan's own size is known
+  if (plan_bytes / 4 < (size_t)(kPlanHeaderWords + num_clusters + 1) + (size_t)d.B * d.s_q + 1)
+    return set_error(MLA_ERR_WORKSPACE_TOO_SMALL, "plan_bytes is less than any plan of these dims");
+  const size_t words = plan_bytes / 4;
+  *room = {words > INT32_MAX ? INT32_MAX : (int)words, part_slots};
+  return MLA_OK;
+}
+
+mla_status_t mla_decode_attn_sized(const mla_dims_t* dims, int32_t cache, const void* q_lat, const void* q_rope,
+                                   const void* kv_pool, const int32_t* block_table, const int32_t* seq_lens,
+                                   const int32_t* draft_masks, const void* plan_dev, size_t plan_bytes,
+                                   int32_t num_clusters, float* o_part, float* lse_part, int32_t part_slots,
+                                   void* o_lat, float* lse_out, int32_t* status, void* stream) {
+  clear_error();
+  MLA_TRY(check_dims(dims));
+  if (cache != MLA_CACHE_BF16 && cache != MLA_CACHE_FP8 && cache != MLA_CACHE_FP4)
+    return set_error(MLA_ERR_INVALID_ARG, "cache must be MLA_CACHE_BF16, MLA_CACHE_FP8 or MLA_CACHE_FP4");
+  if (draft_masks && cache != MLA_CACHE_BF16) return set_error(MLA_ERR_UNSUPPORTED, "draft-tree masks need the bf16 cache");
+  if (draft_masks && dims->causal != 0)
+    return set_error(MLA_ERR_INVALID_ARG, "draft-tree attention needs dims->causal = 0 (plan with kv_len = T)");
+  if (num_clusters < 1 || num_clusters > 4096)
+    return set_error(MLA_ERR_INVALID_ARG, "num_clusters must be in [1, 4096]");
+  MLA_TRY(check_ptr(q_lat, "q_lat"));
+  MLA_TRY(check_ptr(q_rope, "q_rope"));
+  MLA_TRY(check_ptr(kv_pool, "kv_pool"));
+  MLA_TRY(check_words(block_table, "block_table"));
+  MLA_TRY(check_words(seq_lens, "seq_lens"));
+  MLA_TRY(check_optional_words(draft_masks, "draft_masks"));
+  MLA_TRY(check_ptr(o_lat, "o_lat"));
+  MLA_TRY(check_optional_words(lse_out, "lse_out"));
+  MLA_TRY(check_optional_words(status, "status"));
+  PlanRoom room;
+  MLA_TRY(check_sized(*dims, plan_dev, plan_bytes, num_clusters, o_part, lse_part, part_slots, &room));
+  const int32_t* plan = static_cast<const int32_t*>(plan_dev);
+  if (cache == MLA_CACHE_BF16)
+    return launch_decode_attn(*dims, q_lat, q_rope, kv_pool, block_table, seq_lens, draft_masks, plan, num_clusters,
+                              o_part, lse_part, room, o_lat, lse_out, status, stream);
+  return (cache == MLA_CACHE_FP8 ? launch_decode_attn_fp8cache : launch_decode_attn_fp4cache)(
+      *dims, q_lat, q_rope, kv_pool, block_table, seq_lens, plan, num_clusters, o_part, lse_part, room, o_lat, lse_out,
+      status, stream);
+}
+
+mla_status_t mla_combine_sized(const mla_dims_t* dims, const void* plan_dev, size_t plan_bytes, const float* o_part,
+                               const float* lse_part, int32_t part_slots, void* o_lat, float* lse_out,
+                               int32_t* status, void* stream) {
+  clear_error();
+  MLA_TRY(check_dims(dims));
+  MLA_TRY(check_ptr(o_lat, "o_lat"));
+  MLA_TRY(check_optional_words(lse_out, "lse_out"));
+  MLA_TRY(check_optional_words(status, "status"));
+  if (!o_part || !lse_part) return set_error(MLA_ERR_INVALID_ARG, "o_part / lse_part is NULL");
+  PlanRoom room;
+  MLA_TRY(check_sized(*dims, plan_dev, plan_bytes, 1, o_part, lse_part, part_slots, &room));
+  return launch_combine(*dims, static_cast<const int32_t*>(plan_dev), dims->B * dims->s_q, o_part, lse_part, room,
+                        o_lat, lse_out, status, stream);
 }
 
 mla_status_t mla_decode_attn_combine_noalloc(const mla_dims_t* dims, const void* q_lat, const void* q_rope,

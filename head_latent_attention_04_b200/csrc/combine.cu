@@ -34,10 +34,16 @@ template <int G, int P>
 __global__ void __launch_bounds__(kCombineThreads, G == 4 ? 1 : 2)
 mla_combine_kernel(const int32_t* __restrict__ plan, const float* __restrict__ o_part,
                    const float* __restrict__ lse_part, __nv_bfloat16* __restrict__ o_lat,
-                   float* __restrict__ lse_out, int n_heads) {
+                   float* __restrict__ lse_out, int n_heads, PlanRoom room, int32_t* status) {
   ptx::griddep_wait();   // the attention kernel's partials are complete and visible
   ptx::griddep_launch_dependents();
   const int n = blockIdx.x;
+  // the plan must be one for these rows and heads, and its slots in the buffers (as in the attention kernels)
+  if (plan[kHdrMagic] != kPlanMagic || plan[kHdrNumRows] != (int)gridDim.x || plan[kHdrHeads] != n_heads ||
+      plan[kHdrTotalWords] > room.plan_words || plan[kHdrNumSlots] > room.part_slots) {
+    if (n == 0 && blockIdx.y == 0 && threadIdx.x == 0 && status) atomicOr(status, MLA_STATUS_BAD_PLAN);
+    return;
+  }
   const int h = threadIdx.x & 127;
   const int grp = threadIdx.x >> 7;
   if (h >= n_heads) return;
@@ -125,8 +131,8 @@ __global__ void mla_gather_pages_kernel(const uint4* __restrict__ pool, const in
 }  // namespace
 
 mla_status_t launch_combine(const mla_dims_t& d, const int32_t* plan_dev, int32_t n_rows,
-                            const float* o_part, const float* lse_part, void* o_lat,
-                            float* lse_out, void* stream) {
+                            const float* o_part, const float* lse_part, PlanRoom room, void* o_lat,
+                            float* lse_out, int32_t* status, void* stream) {
   // Column groups per thread: the smallest G with n_rows x 32 / G blocks within
   // about one wave (2 blocks of 512 threads per SM).
   static const int sms = [] {
@@ -144,9 +150,9 @@ mla_status_t launch_combine(const mla_dims_t& d, const int32_t* plan_dev, int32_
   auto bf = static_cast<__nv_bfloat16*>(o_lat);
   cudaError_t e;
   switch (G) {
-    case 1: e = launch_pdl(mla_combine_kernel<1, 4>, grid, dim3(kCombineThreads), 0, stream, plan_dev, o_part, lse_part, bf, lse_out, d.n_heads); break;
-    case 2: e = launch_pdl(mla_combine_kernel<2, 2>, grid, dim3(kCombineThreads), 0, stream, plan_dev, o_part, lse_part, bf, lse_out, d.n_heads); break;
-    default: e = launch_pdl(mla_combine_kernel<4, 1>, grid, dim3(kCombineThreads), 0, stream, plan_dev, o_part, lse_part, bf, lse_out, d.n_heads); break;
+    case 1: e = launch_pdl(mla_combine_kernel<1, 4>, grid, dim3(kCombineThreads), 0, stream, plan_dev, o_part, lse_part, bf, lse_out, d.n_heads, room, status); break;
+    case 2: e = launch_pdl(mla_combine_kernel<2, 2>, grid, dim3(kCombineThreads), 0, stream, plan_dev, o_part, lse_part, bf, lse_out, d.n_heads, room, status); break;
+    default: e = launch_pdl(mla_combine_kernel<4, 1>, grid, dim3(kCombineThreads), 0, stream, plan_dev, o_part, lse_part, bf, lse_out, d.n_heads, room, status); break;
   }
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return set_error(MLA_ERR_CUDA, "combine launch: %s", cudaGetErrorString(e));

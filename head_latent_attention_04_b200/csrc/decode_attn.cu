@@ -115,6 +115,7 @@ struct DecodeParams {
   float* lse_out;               // [N][H] or null
   int32_t* status;
   int n_heads, max_blocks, num_blocks, s_q, causal, B, n_rows, num_clusters;
+  PlanRoom room;
   float scale_log2;             // scale * log2(e)
   uint64_t wait_ns;             // limit of every protocol wait (drains of issued work use the default)
   uint32_t zero;                // 0, read at run time (see the release of the peer tile)
@@ -300,7 +301,8 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_consta
                        plan[kHdrNumRows] == p.n_rows && plan[kHdrHeads] == p.n_heads &&
                        plan[kHdrB] == p.B && plan[kHdrSq] == p.s_q &&
                        plan[kHdrMaxBlocks] == p.max_blocks && plan[kHdrCausal] == (p.causal ? 1 : 0) &&
-                       plan[kHdrOffCluster] == off_cluster && plan[kHdrOffItems] == off_items;
+                       plan[kHdrOffCluster] == off_cluster && plan[kHdrOffItems] == off_items &&
+                       plan[kHdrTotalWords] <= p.room.plan_words && plan[kHdrNumSlots] <= p.room.part_slots;
   const int it_begin = plan_ok ? it_begin_raw : 0;
   const int it_end = plan_ok ? it_end_raw : 0;
   if (!plan_ok && threadIdx.x == 0 && rank == 0 && cid == 0) report(p.status, MLA_STATUS_BAD_PLAN);
@@ -927,7 +929,7 @@ template <bool kFp8, bool kTree>
 mla_status_t launch_decode_impl(const mla_dims_t& d, const void* q_lat, const void* q_rope,
                                 const void* kv_pool, const int32_t* block_table,
                                 const int32_t* seq_lens, const int32_t* draft_masks, const int32_t* plan_dev,
-                                int32_t num_clusters, float* o_part, float* lse_part,
+                                int32_t num_clusters, float* o_part, float* lse_part, PlanRoom room,
                                 void* o_lat, float* lse_out, int32_t* status, void* stream) {
   // The pool as (column, row within the block, block): a box may start at a
   // negative row, which the TMA fills with zeros (the shifted last page).
@@ -982,6 +984,7 @@ mla_status_t launch_decode_impl(const mla_dims_t& d, const void* q_lat, const vo
   p.B = d.B;
   p.n_rows = N;
   p.num_clusters = num_clusters;
+  p.room = room;
   p.scale_log2 = d.scale * 1.4426950408889634f;
   p.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   p.zero = 0;
@@ -1001,22 +1004,22 @@ mla_status_t launch_decode_impl(const mla_dims_t& d, const void* q_lat, const vo
 mla_status_t launch_decode_attn(const mla_dims_t& d, const void* q_lat, const void* q_rope,
                                 const void* kv_pool, const int32_t* block_table,
                                 const int32_t* seq_lens, const int32_t* draft_masks, const int32_t* plan_dev,
-                                int32_t num_clusters, float* o_part, float* lse_part,
+                                int32_t num_clusters, float* o_part, float* lse_part, PlanRoom room,
                                 void* o_lat, float* lse_out, int32_t* status, void* stream) {
   if (draft_masks)
     return launch_decode_impl<false, true>(d, q_lat, q_rope, kv_pool, block_table, seq_lens, draft_masks, plan_dev,
-                                           num_clusters, o_part, lse_part, o_lat, lse_out, status, stream);
+                                           num_clusters, o_part, lse_part, room, o_lat, lse_out, status, stream);
   return launch_decode_impl<false, false>(d, q_lat, q_rope, kv_pool, block_table, seq_lens, nullptr, plan_dev,
-                                          num_clusters, o_part, lse_part, o_lat, lse_out, status, stream);
+                                          num_clusters, o_part, lse_part, room, o_lat, lse_out, status, stream);
 }
 
 mla_status_t launch_decode_attn_fp8cache(const mla_dims_t& d, const void* q_lat, const void* q_rope,
                                          const void* kv_pool_fp8, const int32_t* block_table,
                                          const int32_t* seq_lens, const int32_t* plan_dev, int32_t num_clusters,
-                                         float* o_part, float* lse_part, void* o_lat, float* lse_out,
+                                         float* o_part, float* lse_part, PlanRoom room, void* o_lat, float* lse_out,
                                          int32_t* status, void* stream) {
   return launch_decode_impl<true, false>(d, q_lat, q_rope, kv_pool_fp8, block_table, seq_lens, nullptr, plan_dev,
-                                         num_clusters, o_part, lse_part, o_lat, lse_out, status, stream);
+                                         num_clusters, o_part, lse_part, room, o_lat, lse_out, status, stream);
 }
 
 void set_decode_wait_limit_ns(int64_t ns) {

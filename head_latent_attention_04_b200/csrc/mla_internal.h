@@ -36,6 +36,13 @@ void clear_error();
 mla_status_t build_plan(const mla_dims_t& d, const int32_t* seq_lens, int32_t num_clusters,
                         int32_t* plan, int64_t plan_words, int32_t* num_slots_out);
 
+// What the buffers of a split-KV plan hold.  The kernels compare it with the plan's header, which
+// only the device sees, and do nothing for a plan that needs more (MLA_STATUS_BAD_PLAN).
+struct PlanRoom {
+  int plan_words;   // int32 words of the plan's buffer
+  int part_slots;   // partial slots of o_part and lse_part (0 when either is NULL)
+};
+
 // Kernel launchers (defined in the .cu files); each returns MLA_OK or MLA_ERR_CUDA.
 mla_status_t launch_absorb_q(const void* q_nope, const void* w_uk, void* q_lat, int n_tokens,
                              int n_heads, void* stream);
@@ -52,14 +59,14 @@ mla_status_t launch_out_uv_fp8(const void* o_lat, const void* w_codes, const flo
 mla_status_t launch_decode_attn(const mla_dims_t& d, const void* q_lat, const void* q_rope,
                                 const void* kv_pool, const int32_t* block_table,
                                 const int32_t* seq_lens, const int32_t* draft_masks, const int32_t* plan_dev,
-                                int32_t num_clusters, float* o_part, float* lse_part,
+                                int32_t num_clusters, float* o_part, float* lse_part, PlanRoom room,
                                 void* o_lat, float* lse_out, int32_t* status, void* stream);
 // The same kernel on an FP8 latent cache (rows of 656 bytes: 512 E4M3 codes,
 // 4 fp32 block scales, 64 bf16 k_rope).  No draft-tree masks.
 mla_status_t launch_decode_attn_fp8cache(const mla_dims_t& d, const void* q_lat, const void* q_rope,
                                          const void* kv_pool_fp8, const int32_t* block_table,
                                          const int32_t* seq_lens, const int32_t* plan_dev, int32_t num_clusters,
-                                         float* o_part, float* lse_part, void* o_lat, float* lse_out,
+                                         float* o_part, float* lse_part, PlanRoom room, void* o_lat, float* lse_out,
                                          int32_t* status, void* stream);
 // bf16 cache rows [n][576] -> FP8 pool slots (flat token index block * 64 + row).
 mla_status_t launch_kv_quantize_fp8(const void* kv, const int32_t* slots, long long n, void* pool_fp8,
@@ -72,7 +79,7 @@ mla_status_t launch_kv_dequantize_fp4(const void* pool_fp4, const int32_t* slots
 mla_status_t launch_decode_attn_fp4cache(const mla_dims_t& d, const void* q_lat, const void* q_rope,
                                          const void* kv_pool_fp4, const int32_t* block_table,
                                          const int32_t* seq_lens, const int32_t* plan_dev, int32_t num_clusters,
-                                         float* o_part, float* lse_part, void* o_lat, float* lse_out,
+                                         float* o_part, float* lse_part, PlanRoom room, void* o_lat, float* lse_out,
                                          int32_t* status, void* stream);
 void set_decode_fp4_wait_limit_ns(int64_t ns);
 mla_status_t launch_build_tables(int B, const int32_t* cached_lens, const int32_t* new_lens, int max_blocks,
@@ -89,8 +96,8 @@ mla_status_t launch_select_pages(const mla_dims_t& d, const void* q_lat, const v
                                  int n_first, int n_recent, float* scores, int32_t* sel_table, int32_t* sel_lens,
                                  int32_t* sel_pages, int num_clusters, int32_t* plan, int32_t* status, void* stream);
 mla_status_t launch_combine(const mla_dims_t& d, const int32_t* plan_dev, int32_t n_rows,
-                            const float* o_part, const float* lse_part, void* o_lat,
-                            float* lse_out, void* stream);
+                            const float* o_part, const float* lse_part, PlanRoom room, void* o_lat,
+                            float* lse_out, int32_t* status, void* stream);
 mla_status_t launch_prefill_up_proj(const void* kv_pool, const int32_t* block_row, int T, int num_blocks,
                                     const void* w_uk, const void* w_uv, int n_heads, void* k_out, void* v_out,
                                     void* stream);

@@ -111,13 +111,14 @@ mla_status_t decode_attn_combine_noalloc(const mla_dims_t& d, const void* q_lat,
   float* lse_part = reinterpret_cast<float*>(b + plan_region);
   float* o_part = reinterpret_cast<float*>(b + plan_region + lse_region);
 
+  const PlanRoom room = {(int)words, (int)slots};
   cudaError_t e = cudaMemcpyAsync(plan_dev, plan_host, words * 4, cudaMemcpyHostToDevice, s);
   if (e != cudaSuccess) return set_error(MLA_ERR_CUDA, "plan copy: %s", cudaGetErrorString(e));
   st = launch_decode_attn(d, q_lat, q_rope, kv_pool, block_table, seq_lens, nullptr, plan_dev, num_clusters, o_part,
-                          lse_part, o_lat, lse_out, status, stream);
+                          lse_part, room, o_lat, lse_out, status, stream);
   if (st != MLA_OK) return st;
   if (slots > 0)
-    st = launch_combine(d, plan_dev, d.B * d.s_q, o_part, lse_part, o_lat, lse_out, stream);
+    st = launch_combine(d, plan_dev, d.B * d.s_q, o_part, lse_part, room, o_lat, lse_out, status, stream);
   return st;
 }
 

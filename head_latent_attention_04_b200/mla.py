@@ -35,7 +35,8 @@ EXPORTS = ("mla_version", "mla_last_error_string", "mla_absorb_q", "mla_out_uv",
            "mla_out_uv_fp8", "mla_set_wait_limit_ns", "mla_decode_attn_tree", "mla_prefill_up_proj",
            "mla_prefill_attn", "mla_qkv_a_proj", "mla_q_up_absorb", "mla_decode_attn_fp8cache",
            "mla_kv_quantize_fp8", "mla_kv_quantize_fp4", "mla_kv_dequantize_fp4", "mla_decode_attn_fp4cache",
-           "mla_build_tables", "mla_plan_device", "mla_summarize_pages", "mla_select_pages")
+           "mla_build_tables", "mla_plan_device", "mla_summarize_pages", "mla_select_pages",
+           "mla_decode_attn_sized", "mla_combine_sized")
 
 
 class MlaDims(ctypes.Structure):
@@ -60,6 +61,9 @@ for _name, _args in {
     "mla_decode_attn_tree": [_pdims, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp],
     "mla_decode_attn_fp8cache": [_pdims, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp],
     "mla_kv_quantize_fp8": [_vp, _vp, ctypes.c_int64, _vp, _i32, _vp, _vp],
+    "mla_decode_attn_sized": [_pdims, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i32, _vp, _vp, _i32, _vp, _vp, _vp,
+                              _vp],
+    "mla_combine_sized": [_pdims, _vp, _sz, _vp, _vp, _i32, _vp, _vp, _vp, _vp],
     "mla_kv_quantize_fp4": [_vp, _vp, ctypes.c_int64, _vp, _i32, _vp, _vp],
     "mla_kv_dequantize_fp4": [_vp, _vp, ctypes.c_int64, _vp, _i32, _vp, _vp],
     "mla_decode_attn_fp4cache": [_pdims, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp],
@@ -289,22 +293,45 @@ def out_uv_fp8(o_lat: torch.Tensor, w: Fp8Weight, out: torch.Tensor | None = Non
     return out
 
 
+def _room(dims, num_clusters, plan_dev, o_part, lse_part):
+    """(bytes of the plan's buffer, partial slots that both workspaces hold): the kernels
+    refuse a plan that needs more (STATUS_BAD_PLAN).  Raw addresses are taken to
+    have plan_size's sizes."""
+    H, N = dims.n_heads, dims.B * dims.s_q
+    if isinstance(plan_dev, int):
+        plan_bytes = 4 * _plan_words(N, num_clusters)
+    else:
+        plan_bytes = 0 if plan_dev is None else plan_dev.numel() * plan_dev.element_size()
+    if o_part is None or lse_part is None:
+        return plan_bytes, 0
+    bound = num_clusters + N
+    return plan_bytes, min(bound if isinstance(o_part, int) else o_part.numel() // (H * 512),
+                           bound if isinstance(lse_part, int) else lse_part.numel() // H)
+
+
+def _decode_attn(what, cache, dims, q_lat, q_rope, kv_pool, block_table, seq_lens, draft_masks, plan_dev, num_clusters,
+                 o_part, lse_part, o_lat, lse_out, status, stream):
+    plan_bytes, slots = _room(dims, num_clusters, plan_dev, o_part, lse_part)
+    _check(_lib.mla_decode_attn_sized(ctypes.byref(dims), CACHE_KINDS[cache], _ptr(q_lat), _ptr(q_rope), _ptr(kv_pool),
+                                      _ptr(block_table), _ptr(seq_lens), _ptr(draft_masks), _ptr(plan_dev), plan_bytes,
+                                      num_clusters, _ptr(o_part), _ptr(lse_part), slots, _ptr(o_lat), _ptr(lse_out),
+                                      _ptr(status), _stream(stream)), what)
+
+
 def decode_attn(dims, q_lat, q_rope, kv_pool, block_table, seq_lens, plan_dev, num_clusters,
                 o_part, lse_part, o_lat, lse_out=None, status=None, stream=None):
-    _check(_lib.mla_decode_attn(ctypes.byref(dims), _ptr(q_lat), _ptr(q_rope), _ptr(kv_pool),
-                                _ptr(block_table), _ptr(seq_lens), _ptr(plan_dev), num_clusters,
-                                _ptr(o_part), _ptr(lse_part), _ptr(o_lat), _ptr(lse_out),
-                                _ptr(status), _stream(stream)), "mla_decode_attn")
+    _decode_attn("mla_decode_attn", "bf16", dims, q_lat, q_rope, kv_pool, block_table, seq_lens, None, plan_dev,
+                 num_clusters, o_part, lse_part, o_lat, lse_out, status, stream)
 
 
 def decode_attn_tree(dims, q_lat, q_rope, kv_pool, block_table, seq_lens, draft_masks, plan_dev, num_clusters,
                      o_part, lse_part, o_lat, lse_out=None, status=None, stream=None):
     """decode_attn for drafts that form a tree: ``draft_masks`` int32 [B][s_q]
     (device), bit j of row i = draft j visible to query i (dims.causal must be 0)."""
-    _check(_lib.mla_decode_attn_tree(ctypes.byref(dims), _ptr(q_lat), _ptr(q_rope), _ptr(kv_pool),
-                                     _ptr(block_table), _ptr(seq_lens), _ptr(draft_masks), _ptr(plan_dev),
-                                     num_clusters, _ptr(o_part), _ptr(lse_part), _ptr(o_lat), _ptr(lse_out),
-                                     _ptr(status), _stream(stream)), "mla_decode_attn_tree")
+    if draft_masks is None:
+        raise ValueError("draft_masks is needed")
+    _decode_attn("mla_decode_attn_tree", "bf16", dims, q_lat, q_rope, kv_pool, block_table, seq_lens, draft_masks,
+                 plan_dev, num_clusters, o_part, lse_part, o_lat, lse_out, status, stream)
 
 
 FP8_ROW_BYTES = 656   # 512 E4M3 codes | 4 fp32 block scales | 64 bf16 k_rope
@@ -314,10 +341,8 @@ def decode_attn_fp8cache(dims, q_lat, q_rope, kv_pool_fp8, block_table, seq_lens
                          o_part, lse_part, o_lat, lse_out=None, status=None, stream=None):
     """decode_attn on an FP8 latent cache: ``kv_pool_fp8`` uint8
     [num_blocks][64][656] as :func:`kv_quantize_fp8` writes it."""
-    _check(_lib.mla_decode_attn_fp8cache(ctypes.byref(dims), _ptr(q_lat), _ptr(q_rope), _ptr(kv_pool_fp8),
-                                         _ptr(block_table), _ptr(seq_lens), _ptr(plan_dev), num_clusters,
-                                         _ptr(o_part), _ptr(lse_part), _ptr(o_lat), _ptr(lse_out),
-                                         _ptr(status), _stream(stream)), "mla_decode_attn_fp8cache")
+    _decode_attn("mla_decode_attn_fp8cache", "fp8", dims, q_lat, q_rope, kv_pool_fp8, block_table, seq_lens, None,
+                 plan_dev, num_clusters, o_part, lse_part, o_lat, lse_out, status, stream)
 
 
 def kv_quantize_fp8(kv, slots, kv_pool_fp8, status=None, stream=None):
@@ -346,15 +371,16 @@ def decode_attn_fp4cache(dims, q_lat, q_rope, kv_pool_fp4, block_table, seq_lens
     [num_blocks][64][416] as :func:`kv_quantize_fp4` writes it."""
     N, H = dims.B * dims.s_q, dims.n_heads
     with _on(q_lat, q_rope, kv_pool_fp4, block_table, seq_lens, plan_dev, o_part, lse_part, o_lat, lse_out, status):
-        _check(_lib.mla_decode_attn_fp4cache(
-            ctypes.byref(dims), _arg(q_lat, "q_lat", torch.bfloat16, N, H, 512),
+        plan_bytes, slots = _room(dims, num_clusters, plan_dev, o_part, lse_part)
+        _check(_lib.mla_decode_attn_sized(
+            ctypes.byref(dims), CACHE_KINDS["fp4"], _arg(q_lat, "q_lat", torch.bfloat16, N, H, 512),
             _arg(q_rope, "q_rope", torch.bfloat16, N, H, 64),
             _arg(kv_pool_fp4, "kv_pool_fp4", torch.uint8, dims.num_blocks, 64, FP4_ROW_BYTES),
             _arg(block_table, "block_table", torch.int32, dims.B, dims.max_blocks_per_seq),
-            _arg(seq_lens, "seq_lens", torch.int32, dims.B), _vec(plan_dev, "plan_dev", torch.int32),
-            num_clusters, _vec(o_part, "o_part", torch.float32),
-            _vec(lse_part, "lse_part", torch.float32), _arg(o_lat, "o_lat", torch.bfloat16, N, H, 512),
-            _arg(lse_out, "lse_out", torch.float32, N, H), _vec(status, "status", torch.int32), _stream(stream)), "mla_decode_attn_fp4cache")
+            _arg(seq_lens, "seq_lens", torch.int32, dims.B), None, _vec(plan_dev, "plan_dev", torch.int32), plan_bytes,
+            num_clusters, _vec(o_part, "o_part", torch.float32), _vec(lse_part, "lse_part", torch.float32), slots,
+            _arg(o_lat, "o_lat", torch.bfloat16, N, H, 512), _arg(lse_out, "lse_out", torch.float32, N, H),
+            _vec(status, "status", torch.int32), _stream(stream)), "mla_decode_attn_fp4cache")
 
 
 def kv_quantize_fp4(kv, slots, kv_pool_fp4, status=None, stream=None):
@@ -504,9 +530,10 @@ def select_pages(dims: MlaDims, q_lat, q_rope, codes, scales, block_table, seq_l
     return sel_table, sel_lens, sel_pages
 
 
-def combine(dims, plan_dev, o_part, lse_part, o_lat, lse_out=None, stream=None):
-    _check(_lib.mla_combine(ctypes.byref(dims), _ptr(plan_dev), _ptr(o_part), _ptr(lse_part),
-                            _ptr(o_lat), _ptr(lse_out), _stream(stream)), "mla_combine")
+def combine(dims, plan_dev, o_part, lse_part, o_lat, lse_out=None, stream=None, status=None):
+    plan_bytes, slots = _room(dims, 4096, plan_dev, o_part, lse_part)
+    _check(_lib.mla_combine_sized(ctypes.byref(dims), _ptr(plan_dev), plan_bytes, _ptr(o_part), _ptr(lse_part), slots,
+                                  _ptr(o_lat), _ptr(lse_out), _ptr(status), _stream(stream)), "mla_combine")
 
 
 def qkv_a_proj(x, w_qkv_a, c_q=None, kv_a=None, stream=None):

@@ -59,8 +59,8 @@ typedef enum {
 #define MLA_STATUS_BAD_BLOCK   0x1   /* block_table entry outside [0, num_blocks): block 0 used */
 #define MLA_STATUS_TIMEOUT     0x2   /* a bounded device wait expired; outputs are invalid */
 #define MLA_STATUS_BAD_SEQLEN  0x4   /* a row's device seq_lens disagrees with the plan: row skipped */
-#define MLA_STATUS_BAD_PLAN    0x8   /* the plan was made for other dims or another cluster count:
-                                        nothing computed */
+#define MLA_STATUS_BAD_PLAN    0x8   /* the plan was made for other dims or another cluster count, or
+                                        needs larger buffers than it was given: nothing computed */
 #define MLA_STATUS_SCORE_RANGE 0x10  /* a partial score of an attended key left the fp16 range
                                         (|x| > 65504) or was not a number: outputs are invalid */
 #define MLA_STATUS_CACHE_RANGE 0x20  /* mla_kv_quantize_fp8: a 128-column block of c_KV has
@@ -209,7 +209,11 @@ mla_status_t mla_plan(const mla_dims_t* dims, const int32_t* seq_lens_host, int3
  *   o_lat        bf16 [N][n_heads][512]       rows not split are written here
  *   lse_out      fp32 [N][n_heads] or NULL    natural-log LSE of the scaled logits
  *   status       int32 [1] or NULL
- * Rows that the plan splits are completed by mla_combine.
+ * Rows that the plan splits are completed by mla_combine.  Give both workspaces in
+ * mla_plan_size's sizes, or at least the num_slots of mla_plan; NULL for either is a workspace
+ * without slots.  A plan that needs more slots is MLA_STATUS_BAD_PLAN (the size itself is
+ * known only to mla_decode_attn_sized; here a workspace that is not NULL is taken to hold
+ * mla_plan_size's slots).
  *
  * Numerics: the two CTAs of a cluster each score half of the 576 columns and
  * exchange their partial scores rounded to fp16; a partial of an attended key
@@ -300,8 +304,7 @@ mla_status_t mla_kv_quantize_fp8(const void* kv, const int32_t* slots, int64_t n
  * Numerics: rows are widened on chip to fp16 (code * scale, rounded once), q_lat is rounded to
  * fp16, P is written as fp16, and the products accumulate in fp32; the RoPE
  * products are bf16, and partial scores are exchanged in fp16 as in
- * mla_decode_attn.  |q_lat| <= 65504 (else MLA_STATUS_SCORE_RANGE).  A plan that splits a
- * row without o_part and lse_part is MLA_STATUS_BAD_PLAN.  All other
+ * mla_decode_attn.  |q_lat| <= 65504 (else MLA_STATUS_SCORE_RANGE).  All other
  * arguments, outputs, status bits and the plan are those of mla_decode_attn;
  * mla_combine completes split rows.  No draft-tree masks.
  */
@@ -430,10 +433,31 @@ mla_status_t mla_select_pages(const mla_dims_t* dims, const void* q_lat, const v
  * mla_combine -- log-sum-exp merge of the split pieces of each split row:
  *   L = log sum_i exp(lse_i),  o_lat = sum_i exp(lse_i - L) * O_i.
  * Reads o_part/lse_part written by mla_decode_attn with the same plan, writes
- * o_lat bf16 [N][n_heads][512] and (if non-NULL) lse_out for split rows only.
+ * o_lat bf16 [N][n_heads][512] and (if non-NULL) lse_out for split rows only.  Does nothing
+ * when the plan is none for these rows and heads.
  */
 mla_status_t mla_combine(const mla_dims_t* dims, const void* plan_dev, const float* o_part, const float* lse_part, void* o_lat,
                          float* lse_out, void* stream);
+
+/*
+ * mla_decode_attn_sized, mla_combine_sized -- the attention (over the pool kind `cache`; draft_masks
+ * as in mla_decode_attn_tree, bf16 cache only, or NULL) and the merge, with the sizes of the plan's
+ * buffer and of the workspaces.  They are what a plan made on the device wants, whose slots
+ * the host does not see: a plan that is longer than plan_bytes or splits rows into more
+ * pieces than part_slots sets MLA_STATUS_BAD_PLAN and nothing is read or written through it.
+ *   plan_bytes   size of plan_dev (a plan made by mla_plan or on the device fits mla_plan_size's)
+ *   part_slots   slots that both hold: o_part part_slots x n_heads x 512 floats, lse_part
+ *                part_slots x n_heads.  0: none, either may then be NULL (mla_combine_sized
+ *                wants them all the same)
+ */
+mla_status_t mla_decode_attn_sized(const mla_dims_t* dims, int32_t cache, const void* q_lat, const void* q_rope,
+                                   const void* kv_pool, const int32_t* block_table, const int32_t* seq_lens,
+                                   const int32_t* draft_masks, const void* plan_dev, size_t plan_bytes,
+                                   int32_t num_clusters, float* o_part, float* lse_part, int32_t part_slots,
+                                   void* o_lat, float* lse_out, int32_t* status, void* stream);
+mla_status_t mla_combine_sized(const mla_dims_t* dims, const void* plan_dev, size_t plan_bytes, const float* o_part,
+                               const float* lse_part, int32_t part_slots, void* o_lat, float* lse_out,
+                               int32_t* status, void* stream);
 
 /*
  * mla_decode_attn_combine_noalloc -- mla_decode_attn followed by mla_combine,
