@@ -38,16 +38,20 @@ mla_combine_kernel(const int32_t* __restrict__ plan, const float* __restrict__ o
   ptx::griddep_wait();   // the attention kernel's partials are complete and visible
   ptx::griddep_launch_dependents();
   const int n = blockIdx.x;
-  // the plan must be one for these rows and heads, and its slots in the buffers (as in the attention kernels)
-  if (plan[kHdrMagic] != kPlanMagic || plan[kHdrNumRows] != (int)gridDim.x || plan[kHdrHeads] != n_heads ||
-      plan[kHdrTotalWords] > room.plan_words || plan[kHdrNumSlots] > room.part_slots) {
+  // the plan must be one for these rows and heads, and its slots in the buffers (as in the attention
+  // kernels; no short-circuit: the words are read together)
+  const bool plan_ok = (plan[kHdrMagic] == kPlanMagic) & (plan[kHdrNumRows] == (int)gridDim.x) &
+                       (plan[kHdrHeads] == n_heads) & (plan[kHdrTotalWords] <= room.plan_words) &
+                       (plan[kHdrNumSlots] <= room.part_slots);
+  const int off_rows = plan[kHdrOffRows];
+  if (!plan_ok) {
     if (n == 0 && blockIdx.y == 0 && threadIdx.x == 0 && status) atomicOr(status, MLA_STATUS_BAD_PLAN);
     return;
   }
   const int h = threadIdx.x & 127;
   const int grp = threadIdx.x >> 7;
   if (h >= n_heads) return;
-  const int32_t* rs = plan + plan[kHdrOffRows];
+  const int32_t* rs = plan + off_rows;
   const int s0 = rs[n], s1 = rs[n + 1];
   if (s1 <= s0) return;   // row written whole by the attention kernel
 

@@ -297,12 +297,13 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_consta
   const int off_cluster = kPlanHeaderWords, off_items = kPlanHeaderWords + p.num_clusters + 1;
   const int32_t* items = plan + off_items;
   const int it_begin_raw = plan[off_cluster + cid], it_end_raw = plan[off_cluster + cid + 1];
-  const bool plan_ok = plan[kHdrMagic] == kPlanMagic && plan[kHdrNumClusters] == p.num_clusters &&
-                       plan[kHdrNumRows] == p.n_rows && plan[kHdrHeads] == p.n_heads &&
-                       plan[kHdrB] == p.B && plan[kHdrSq] == p.s_q &&
-                       plan[kHdrMaxBlocks] == p.max_blocks && plan[kHdrCausal] == (p.causal ? 1 : 0) &&
-                       plan[kHdrOffCluster] == off_cluster && plan[kHdrOffItems] == off_items &&
-                       plan[kHdrTotalWords] <= p.room.plan_words && plan[kHdrNumSlots] <= p.room.part_slots;
+  // (no short-circuit: the words are read together, not one after the other)
+  const bool plan_ok = (plan[kHdrMagic] == kPlanMagic) & (plan[kHdrNumClusters] == p.num_clusters) &
+                       (plan[kHdrNumRows] == p.n_rows) & (plan[kHdrHeads] == p.n_heads) &
+                       (plan[kHdrB] == p.B) & (plan[kHdrSq] == p.s_q) &
+                       (plan[kHdrMaxBlocks] == p.max_blocks) & (plan[kHdrCausal] == (p.causal ? 1 : 0)) &
+                       (plan[kHdrOffCluster] == off_cluster) & (plan[kHdrOffItems] == off_items) &
+                       (plan[kHdrTotalWords] <= p.room.plan_words) & (plan[kHdrNumSlots] <= p.room.part_slots);
   const int it_begin = plan_ok ? it_begin_raw : 0;
   const int it_end = plan_ok ? it_end_raw : 0;
   if (!plan_ok && threadIdx.x == 0 && rank == 0 && cid == 0) report(p.status, MLA_STATUS_BAD_PLAN);
