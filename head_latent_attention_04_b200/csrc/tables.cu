@@ -57,7 +57,8 @@ build_tables_kernel(const TablesParams p) {
   const int head_raw = *p.head_in;
   const int head = head_raw < 0 || head_raw > p.n_free ? p.n_free : head_raw;
   if (head != head_raw && t == 0) report(p.status, MLA_STATUS_NO_SPACE);
-  long long pages_before = 0, asked_before = 0;   // of the requests that are valid, admitted or not
+  long long pages_before = 0;                     // of the requests that are valid, admitted or not
+  long long asked_before = 0;                     // of those that get their pages
   int used = head, tokens_before = 0;             // admitted ones
   if (t == 0) p.cu_new[0] = 0;
   for (int b0 = 0; b0 < p.B; b0 += kThreads) {
@@ -69,8 +70,10 @@ build_tables_kernel(const TablesParams p) {
     const int want = valid ? add : 0;
     long long pages_all, asked_all;
     const long long pages_incl = pages_before + block_scan<long long>(need, ws, &pages_all);
-    const long long asked_incl = asked_before + block_scan<long long>(want, ws, &asked_all);
-    const bool admitted = valid && (want == 0 || ((need == 0 || head + pages_incl <= p.n_free) && asked_incl <= p.max_new));
+    // (a request refused for its blocks asks for no room in the slot map)
+    const bool has_pages = valid && (need == 0 || head + pages_incl <= p.n_free);
+    const long long asked_incl = asked_before + block_scan<long long>(has_pages ? want : 0, ws, &asked_all);
+    const bool admitted = has_pages && (want == 0 || asked_incl <= p.max_new);
     if (b < p.B && !admitted) report(p.status, MLA_STATUS_NO_SPACE);
     int pages_sum = (int)(pages_incl - pages_before), tokens_sum = (int)(asked_incl - asked_before);
     int pages_now = (int)pages_all, tokens_now = (int)asked_all;

@@ -362,6 +362,7 @@ mla_status_t mla_kv_dequantize_fp4(const void* pool_fp4, const int32_t* slots, i
  *                 or a length is negative.  Its seq_lens entry stays at cached_lens (0 if that is
  *                 negative).  Requests are admitted in order: once one does not fit the free list no
  *                 later one gets new blocks, once one does not fit max_new no later one gets tokens.
+ *                 A request that does not fit the free list takes no room in the slot map.
  *                 MLA_STATUS_BAD_BLOCK when a block id read lies outside the pool (its slots are -1)
  * 1 <= B <= 65536.  The arrays must not overlap except as said.
  *

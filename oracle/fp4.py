@@ -105,9 +105,10 @@ def build_tables(cached, new, table, free, head, max_new):
             held = -(-c // PAGE)
             need = -(-(c + n) // PAGE) - held
             pages_asked += need
-            tokens_asked += n
-            if n > 0:
-                admitted = (need == 0 or start + pages_asked <= len(free)) and tokens_asked <= max_new
+            admitted = need == 0 or start + pages_asked <= len(free)
+            if admitted:                       # a request refused for its blocks asks for no room in the slot map
+                tokens_asked += n
+                admitted = n == 0 or tokens_asked <= max_new
         if not admitted:
             no_space = True
             lens.append(max(c, 0))
