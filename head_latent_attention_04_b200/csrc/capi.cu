@@ -383,8 +383,8 @@ mla_status_t mla_decode_attn_fp4cache(const mla_dims_t* dims, const void* q_lat,
                                      o_lat, lse_out, status, stream);
 }
 
-mla_status_t mla_build_tables(int32_t B, const int32_t* cached_lens, const int32_t* new_lens,
-                              int32_t max_blocks_per_seq, int32_t* block_table, const int32_t* free_blocks,
+mla_status_t mla_build_tables_held(int32_t B, const int32_t* cached_lens, const int32_t* new_lens,
+                              int32_t max_blocks_per_seq, int32_t* block_table, int32_t* held_pages, const int32_t* free_blocks,
                               int32_t n_free, const int32_t* free_head, int32_t num_blocks, int32_t max_new,
                               int32_t* seq_lens, int32_t* cu_new, int32_t* slots, int32_t* positions,
                               int32_t* free_head_out, int32_t* status, void* stream) {
@@ -397,6 +397,7 @@ mla_status_t mla_build_tables(int32_t B, const int32_t* cached_lens, const int32
   MLA_TRY(check_words(cached_lens, "cached_lens"));
   MLA_TRY(check_words(new_lens, "new_lens"));
   MLA_TRY(check_words(block_table, "block_table"));
+  MLA_TRY(check_optional_words(held_pages, "held_pages"));
   if (n_free > 0) MLA_TRY(check_words(free_blocks, "free_blocks"));
   MLA_TRY(check_words(free_head, "free_head"));
   MLA_TRY(check_words(seq_lens, "seq_lens"));
@@ -405,8 +406,18 @@ mla_status_t mla_build_tables(int32_t B, const int32_t* cached_lens, const int32
   MLA_TRY(check_optional_words(positions, "positions"));
   MLA_TRY(check_words(free_head_out, "free_head_out"));
   MLA_TRY(check_optional_words(status, "status"));
-  return launch_build_tables(B, cached_lens, new_lens, max_blocks_per_seq, block_table, free_blocks, n_free, free_head,
+  return launch_build_tables(B, cached_lens, new_lens, max_blocks_per_seq, block_table, held_pages, free_blocks, n_free, free_head,
                              num_blocks, max_new, seq_lens, cu_new, slots, positions, free_head_out, status, stream);
+}
+
+mla_status_t mla_build_tables(int32_t B, const int32_t* cached_lens, const int32_t* new_lens,
+                              int32_t max_blocks_per_seq, int32_t* block_table, const int32_t* free_blocks,
+                              int32_t n_free, const int32_t* free_head, int32_t num_blocks, int32_t max_new,
+                              int32_t* seq_lens, int32_t* cu_new, int32_t* slots, int32_t* positions,
+                              int32_t* free_head_out, int32_t* status, void* stream) {
+  return mla_build_tables_held(B, cached_lens, new_lens, max_blocks_per_seq, block_table, nullptr, free_blocks, n_free,
+                               free_head, num_blocks, max_new, seq_lens, cu_new, slots, positions, free_head_out,
+                               status, stream);
 }
 
 mla_status_t mla_plan_device(const mla_dims_t* dims, const int32_t* seq_lens, int32_t num_clusters, void* plan_dev,

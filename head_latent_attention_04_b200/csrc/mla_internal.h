@@ -83,7 +83,7 @@ mla_status_t launch_decode_attn_fp4cache(const mla_dims_t& d, const void* q_lat,
                                          int32_t* status, void* stream);
 void set_decode_fp4_wait_limit_ns(int64_t ns);
 mla_status_t launch_build_tables(int B, const int32_t* cached_lens, const int32_t* new_lens, int max_blocks,
-                                 int32_t* block_table, const int32_t* free_blocks, int n_free,
+                                 int32_t* block_table, int32_t* held_pages, const int32_t* free_blocks, int n_free,
                                  const int32_t* free_head, int num_blocks, int max_new, int32_t* seq_lens,
                                  int32_t* cu_new, int32_t* slots, int32_t* positions, int32_t* free_head_out,
                                  int32_t* status, void* stream);

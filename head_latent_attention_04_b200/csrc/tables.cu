@@ -30,6 +30,7 @@ struct TablesParams {
   const int32_t* cached;
   const int32_t* fresh;
   int32_t* table;
+  int32_t* held;   // pages that the rows of the table hold, or null (then those of the cached tokens)
   const int32_t* free_blocks;
   const int32_t* head_in;
   int32_t* seq_lens;
@@ -64,9 +65,10 @@ build_tables_kernel(const TablesParams p) {
   for (int b0 = 0; b0 < p.B; b0 += kThreads) {
     const int b = b0 + t;
     const int old = b < p.B ? p.cached[b] : 0, add = b < p.B ? p.fresh[b] : 0;
-    const bool valid = old >= 0 && add >= 0 && (long long)old + add <= (long long)p.max_blocks * kPage;
-    const int held = valid ? (old + kPage - 1) / kPage : 0;
-    const int need = valid ? (old + add + kPage - 1) / kPage - held : 0;
+    const int in_row = p.held && b < p.B ? p.held[b] : 0;
+    const bool valid = old >= 0 && add >= 0 && (long long)old + add <= (long long)p.max_blocks * kPage && in_row <= p.max_blocks;
+    const int held = valid ? max(in_row, (old + kPage - 1) / kPage) : 0;
+    const int need = valid ? max((old + add + kPage - 1) / kPage - held, 0) : 0;
     const int want = valid ? add : 0;
     long long pages_all, asked_all;
     const long long pages_incl = pages_before + block_scan<long long>(need, ws, &pages_all);
@@ -91,6 +93,7 @@ build_tables_kernel(const TablesParams p) {
     if (b < p.B) {
       p.cu_new[b + 1] = tokens_before + tokens_sum;
       p.seq_lens[b] = admitted ? old + add : max(old, 0);
+      if (p.held && admitted) p.held[b] = held + need;
     }
     __syncthreads();
     // Pages, then tokens: one each per thread, or four neighbours when there are more
@@ -227,12 +230,12 @@ plan_kernel(const PlanShape p, const int32_t* seq_lens, int32_t* plan, int32_t* 
 constexpr int kOneBlockTokens = 7168;
 
 mla_status_t launch_build_tables(int B, const int32_t* cached_lens, const int32_t* new_lens, int max_blocks,
-                                 int32_t* block_table, const int32_t* free_blocks, int n_free,
+                                 int32_t* block_table, int32_t* held_pages, const int32_t* free_blocks, int n_free,
                                  const int32_t* free_head, int num_blocks, int max_new, int32_t* seq_lens,
                                  int32_t* cu_new, int32_t* slots, int32_t* positions, int32_t* free_head_out,
                                  int32_t* status, void* stream) {
-  TablesParams p = {B, max_blocks, n_free, num_blocks, max_new, cached_lens, new_lens, block_table, free_blocks,
-                    free_head, seq_lens, cu_new, slots, positions, free_head_out, status,
+  TablesParams p = {B, max_blocks, n_free, num_blocks, max_new, cached_lens, new_lens, block_table, held_pages,
+                    free_blocks, free_head, seq_lens, cu_new, slots, positions, free_head_out, status,
                     max_new <= kOneBlockTokens ? 1 : 0};
   cudaError_t e = launch_pdl(build_tables_kernel, dim3(1), dim3(kThreads), 0, stream, p);
   if (e == cudaSuccess && !p.fill) {

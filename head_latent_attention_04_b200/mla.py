@@ -36,7 +36,7 @@ EXPORTS = ("mla_version", "mla_last_error_string", "mla_absorb_q", "mla_out_uv",
            "mla_prefill_attn", "mla_qkv_a_proj", "mla_q_up_absorb", "mla_decode_attn_fp8cache",
            "mla_kv_quantize_fp8", "mla_kv_quantize_fp4", "mla_kv_dequantize_fp4", "mla_decode_attn_fp4cache",
            "mla_build_tables", "mla_plan_device", "mla_summarize_pages", "mla_select_pages",
-           "mla_decode_attn_sized", "mla_combine_sized")
+           "mla_decode_attn_sized", "mla_combine_sized", "mla_build_tables_held")
 
 
 class MlaDims(ctypes.Structure):
@@ -68,6 +68,7 @@ for _name, _args in {
     "mla_kv_dequantize_fp4": [_vp, _vp, ctypes.c_int64, _vp, _i32, _vp, _vp],
     "mla_decode_attn_fp4cache": [_pdims, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp],
     "mla_build_tables": [_i32, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+    "mla_build_tables_held": [_i32, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
     "mla_plan_device": [_pdims, _vp, _i32, _vp, _sz, _vp, _vp],
     "mla_summarize_pages": [_vp, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp],
     "mla_select_pages": [_pdims, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp,
@@ -435,13 +436,19 @@ class BatchTables:
 
 
 def build_tables(cached_lens, new_lens, block_table, free_blocks, free_head, max_new: int, num_blocks: int,
-                 out: BatchTables | None = None, status=None, stream=None) -> BatchTables:
+                 out: BatchTables | None = None, status=None, stream=None, held_pages=None) -> BatchTables:
     """Block tables and slot maps of a step on the GPU, from the requests' lengths.
 
     ``cached_lens``, ``new_lens`` int32 [B]; ``block_table`` int32 [B][max_blocks]
     gains the new pages' blocks, taken from ``free_blocks[free_head[0]:]`` in
     request order.  ``out.seq_lens`` may be ``cached_lens`` and
     ``out.free_head`` may be ``free_head``: a captured step then moves on by itself.
+
+    ``held_pages`` (int32 [B], updated in place; zeros for new requests) counts the
+    pages whose blocks each row of the table holds.  Give it where ``cached_lens`` can
+    fall (rejected drafts): without it a request is taken to hold the pages of its
+    cached tokens only, and a page that only the rejected tokens reached is given a
+    second block while the first is lost.
     """
     B, width = cached_lens.shape[0], block_table.shape[-1]
     i32 = torch.int32
@@ -451,17 +458,17 @@ def build_tables(cached_lens, new_lens, block_table, free_blocks, free_head, max
         at = out.seq_lens.data_ptr()              # the five arrays of empty(), one behind the other
         lens, cu, slots, positions = at, at + 4 * B, at + 8 * B + 4, at + 8 * B + 4 + 4 * max_new
         head_out = positions + 4 * max_new
-        device = _on(block_table, cached_lens, new_lens, free_blocks, free_head, status)
+        device = _on(block_table, cached_lens, new_lens, free_blocks, free_head, status, held_pages)
     else:
         lens, cu = _arg(out.seq_lens, "seq_lens", i32, B), _arg(out.cu_new, "cu_new", i32, B + 1)
         slots, positions = _arg(out.slots, "slots", i32, max_new), _arg(out.positions, "positions", i32, max_new)
         head_out = _arg(out.free_head, "free_head", i32, 1)
-        device = _on(block_table, cached_lens, new_lens, free_blocks, free_head, status, out.seq_lens, out.cu_new,
-                     out.slots, out.positions, out.free_head)
+        device = _on(block_table, cached_lens, new_lens, free_blocks, free_head, status, held_pages, out.seq_lens,
+                     out.cu_new, out.slots, out.positions, out.free_head)
     with device:
-        _check(_lib.mla_build_tables(
+        _check(_lib.mla_build_tables_held(
             B, _arg(cached_lens, "cached_lens", i32, B), _arg(new_lens, "new_lens", i32, B), width,
-            _arg(block_table, "block_table", i32, B, width), _vec(free_blocks, "free_blocks", i32), free_blocks.numel(),
+            _arg(block_table, "block_table", i32, B, width), _arg(held_pages, "held_pages", i32, B), _vec(free_blocks, "free_blocks", i32), free_blocks.numel(),
             _arg(free_head, "free_head", i32, 1), num_blocks, max_new, lens, cu, slots, positions, head_out,
             _vec(status, "status", i32), _stream(stream)), "mla_build_tables")
     return out

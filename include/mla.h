@@ -365,6 +365,17 @@ mla_status_t mla_kv_dequantize_fp4(const void* pool_fp4, const int32_t* slots, i
  *                 A request that does not fit the free list takes no room in the slot map.
  *                 MLA_STATUS_BAD_BLOCK when a block id read lies outside the pool (its slots are -1)
  * 1 <= B <= 65536.  The arrays must not overlap except as said.
+ * A request is taken to hold the pages of its cached tokens and no others.  Where cached_lens can
+ * fall between steps (rejected drafts), a page that only they reached would be given a second
+ * block and the first would be lost: use mla_build_tables_held.
+ *
+ * mla_build_tables_held -- mla_build_tables for lengths that may fall:
+ *   held_pages  int32 [B], in and out, or NULL: the pages whose blocks the request's table row
+ *               holds, at least those of its cached tokens (a smaller entry counts as that many).
+ *               Blocks are taken for pages behind them only, and an admitted request's entry becomes
+ *               the pages it holds now.  Zero for a new request; when one ends, its row's first
+ *               held_pages[b] entries are the blocks to return.  An entry beyond
+ *               max_blocks_per_seq refuses the request (MLA_STATUS_NO_SPACE)
  *
  * mla_plan_device -- mla_plan on the GPU: the same plan, word for word, from
  * device lengths, so that a captured decode step follows them.
@@ -381,6 +392,12 @@ mla_status_t mla_build_tables(int32_t B, const int32_t* cached_lens, const int32
                               int32_t n_free, const int32_t* free_head, int32_t num_blocks, int32_t max_new,
                               int32_t* seq_lens, int32_t* cu_new, int32_t* slots, int32_t* positions,
                               int32_t* free_head_out, int32_t* status, void* stream);
+mla_status_t mla_build_tables_held(int32_t B, const int32_t* cached_lens, const int32_t* new_lens,
+                                   int32_t max_blocks_per_seq, int32_t* block_table, int32_t* held_pages,
+                                   const int32_t* free_blocks, int32_t n_free, const int32_t* free_head,
+                                   int32_t num_blocks, int32_t max_new, int32_t* seq_lens, int32_t* cu_new,
+                                   int32_t* slots, int32_t* positions, int32_t* free_head_out, int32_t* status,
+                                   void* stream);
 mla_status_t mla_plan_device(const mla_dims_t* dims, const int32_t* seq_lens, int32_t num_clusters, void* plan_dev,
                              size_t plan_bytes, int32_t* status, void* stream);
 

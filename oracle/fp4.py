@@ -89,8 +89,9 @@ def select(q, pcodes, pscales, kv_len, k, n_first, n_recent):
     return sorted(list(range(n_first)) + middle[:k - n_first - n_recent] + list(range(count - n_recent, count)))
 
 
-def build_tables(cached, new, table, free, head, max_new):
-    """Request by request; returns (table, seq_lens, cu_new, slots, positions, head, no_space)."""
+def build_tables(cached, new, table, free, head, max_new, held_pages=None):
+    """Request by request; returns (table, seq_lens, cu_new, slots, positions, head, no_space).
+    ``held_pages`` (a list, updated): pages whose blocks the rows hold, at least those of the cached tokens."""
     table = [list(r) for r in table]
     width = len(table[0])
     lens, cu, slots, pos = [], [0], [], []
@@ -99,11 +100,12 @@ def build_tables(cached, new, table, free, head, max_new):
         head, no_space = len(free), True
     pages_asked, tokens_asked, start = 0, 0, head
     for b, (c, n) in enumerate(zip(cached, new)):
-        valid = c >= 0 and n >= 0 and c + n <= width * PAGE
+        in_row = held_pages[b] if held_pages else 0
+        valid = c >= 0 and n >= 0 and c + n <= width * PAGE and in_row <= width
         admitted = valid
         if valid:
-            held = -(-c // PAGE)
-            need = -(-(c + n) // PAGE) - held
+            held = max(in_row, -(-c // PAGE))
+            need = max(-(-(c + n) // PAGE) - held, 0)
             pages_asked += need
             admitted = need == 0 or start + pages_asked <= len(free)
             if admitted:                       # a request refused for its blocks asks for no room in the slot map
@@ -116,6 +118,8 @@ def build_tables(cached, new, table, free, head, max_new):
             for j in range(need):
                 table[b][held + j] = free[head]
                 head += 1
+            if held_pages:
+                held_pages[b] = held + need
             for t in range(c, c + n):
                 slots.append(table[b][t // PAGE] * PAGE + t % PAGE)
                 pos.append(t)
