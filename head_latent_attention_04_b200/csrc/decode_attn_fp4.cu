@@ -28,9 +28,14 @@
 // dimension: CTA r owns latent columns [256r, 256r + 256) and RoPE columns [32r, 32r + 32),
 // computes partial scores over its 288 columns and exchanges them through
 // distributed shared memory in log2 units, rounded to fp16 (16 KB per page
-// each way, one bulk copy counted on the receiver's mbarrier); both CTAs add
-// fp16(S0) + fp16(S1), bit-identical in the pair.  The rounding moves a logit by at most
-// 2^-11 of a partial's size, below the bf16 rounding of the output.
+// each way, one bulk copy counted on the receiver's mbarrier), and both CTAs add the
+// two in fp32.  fp16, because a tile of fp32 each way does not fit beside the rings and
+// doubles the exchange.  What it costs: a logit moves by at most 2^-11 (|p0| + |p1|) in
+// log2 units, p0 and p1 its two partials, so a weight by that times ln 2 (partials of 16:
+// 1 % at worst); two halves that cancel are rounded at their own size.  Measured on 4096
+// random keys, relative Frobenius error of o_lat, of which the output's own rounding is
+// 1.7e-3: logits up to 9 1.8e-3, to 26 2.1e-3, to 84 3.5e-3, to 244 3.6e-3 (with the sum
+// rounded to fp16 as well 2.0e-3, 2.7e-3, 5.3e-3, 4.3e-3, and 1.5 % less time).
 //
 // Two rings, because the cache's bytes are few: four raw half pages (13 KB each:
 // 8 KB of codes, 1 KB of scales, 4 KB of RoPE columns, which the QK product reads there)
@@ -223,26 +228,30 @@ __device__ __forceinline__ void tmem_st16x2_16(uint32_t taddr, const uint32_t (&
       : "memory");
 }
 
-// fp16 pair sum and maximum (round to nearest even; the maximum of -inf and x is x).
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
+// (a.lo + c) + b.lo and the same of the high halves in fp32, for fp16 pairs a and b: the
+// mixed-precision add takes the fp16 operand exactly and rounds the sum once.
+__device__ __forceinline__ void add_f16x2_to_f32(uint32_t a, uint32_t b, float c, float& lo, float& hi) {
+  asm("{\n\t.reg .f16 a0, a1, b0, b1;\n\t.reg .f32 x, y;\n\t"
+      "mov.b32 {a0, a1}, %2;\n\tmov.b32 {b0, b1}, %3;\n\t"
+      "add.rn.f32.f16 x, a0, %4;\n\tadd.rn.f32.f16 y, a1, %4;\n\t"
+      "add.rn.f32.f16 %0, b0, x;\n\tadd.rn.f32.f16 %1, b1, y;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(a), "r"(b), "f"(c));
 }
 
-// (a.lo + c, a.hi + c) in fp32 for an fp16 pair a: the mixed-precision add
-// takes the fp16 operand exactly and rounds the sum once.
-__device__ __forceinline__ void add_f16x2_to_f32(uint32_t a, float c, float& lo, float& hi) {
-  asm("{\n\t.reg .f16 a0, a1;\n\t"
-      "mov.b32 {a0, a1}, %2;\n\t"
-      "add.rn.f32.f16 %0, a0, %3;\n\tadd.rn.f32.f16 %1, a1, %3;\n\t}"
-      : "=f"(lo), "=f"(hi)
-      : "r"(a), "f"(c));
+// Three-input maximum and packed fp32 addition.
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -686,6 +695,7 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
       const int shift_last = kPage - min(last_page_keys(w), kPage);
 
       float m_ref = -CUDART_INF_F, l_run = 0.f;
+      float nb = 0.f;   // -m_ref, or 0 as long as no key was seen
       for (int j = 0; j < n; ++j) {
         const int gj = g + j;
         // full score = fp16(own partial) + fp16(peer partial), identical in both CTAs.
@@ -725,58 +735,67 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
             mbar_arrive_relaxed_cluster(ok_addr);
           }
         }
-        // scores in log2 units: fp16(own) + fp16(peer), summed as fp16 pairs
-        uint32_t s2[16];
+        // Scores in log2 units above the row's reference maximum, (fp16(own) - m_ref) + fp16(peer) in
+        // fp32: the partials' roundings to fp16 are the only ones that count.  (The pair's CTAs
+        // add in different orders, so their references may differ in the last bit: each
+        // normalises its own columns by its own sum.)
+        float sc[32];
         {
           const uint32_t* ow = reinterpret_cast<const uint32_t*>(po);
           const uint32_t* pw = reinterpret_cast<const uint32_t*>(pr);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) s2[k] = hadd2(ow[k], pw[k]);
+          for (int k = 0; k < 16; ++k) add_f16x2_to_f32(ow[k], pw[k], nb, sc[2 * k], sc[2 * k + 1]);
         }
         // masked keys [0, lo) of this page (-inf): the last page's zero fill, or
         // all of them when the device seq_lens disagree with the plan
         const int lo = stale ? kPage : (j == n - 1 ? shift_last : 0);
         if (lo > 32 * c) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            if (32 * c + 2 * k < lo) s2[k] = (s2[k] & 0xffff0000u) | 0xfc00u;
-            if (32 * c + 2 * k + 1 < lo) s2[k] = (s2[k] & 0x0000ffffu) | 0xfc000000u;
-          }
+          for (int k = 0; k < 32; ++k)
+            if (32 * c + k < lo) sc[k] = -CUDART_INF_F;
         }
         float mloc;
         {
-          uint32_t t[8];
+          float t[4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) t[k] = hmax2(s2[k], s2[k + 8]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) t[k] = hmax2(t[k], t[k + 4]);
-          t[0] = hmax2(hmax2(t[0], t[2]), hmax2(t[1], t[3]));
-          const float2 m2 = unpack_f16x2(t[0]);
-          mloc = fmaxf(m2.x, m2.y);
+          for (int k = 0; k < 4; ++k) {
+            t[k] = max3f(sc[8 * k], sc[8 * k + 1], sc[8 * k + 2]);
+            t[k] = max3f(t[k], sc[8 * k + 3], sc[8 * k + 4]);
+            t[k] = max3f(t[k], sc[8 * k + 5], sc[8 * k + 6]);
+          }
+          t[0] = max3f(t[0], sc[7], sc[15]);
+          t[1] = max3f(t[1], sc[23], sc[31]);
+          mloc = fmaxf(max3f(t[0], t[1], t[2]), t[3]);
         }
         const float mx = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 16));
 
         // lazy reference max (log2 domain): move it only when the row max grows by > 2^8
-        const float m_new = fmaxf(m_ref, mx);
-        const bool move = (m_ref == -CUDART_INF_F) ? (m_new != -CUDART_INF_F)
-                                                   : (m_new > m_ref + kRescaleThreshold);
+        const bool first = m_ref == -CUDART_INF_F;
+        const bool move = first ? mx != -CUDART_INF_F : mx > kRescaleThreshold;
         float alpha = 1.f;
-        if (move) {
-          alpha = (m_ref == -CUDART_INF_F) ? 0.f : ex2(m_ref - m_new);
-          m_ref = m_new;
+        if (__any_sync(0xffffffffu, move)) {
+          const float d = move ? -mx : 0.f;
+          if (move) {
+            alpha = first ? 0.f : ex2(-mx);
+            m_ref = first ? mx : m_ref + mx;
+            nb = -m_ref;
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float2 x = add2(make_float2(sc[2 * k], sc[2 * k + 1]), make_float2(d, d));
+            sc[2 * k] = x.x;
+            sc[2 * k + 1] = x.y;
+          }
         }
-        const float nb = (m_ref == -CUDART_INF_F) ? 0.f : -m_ref;
         uint32_t pk[16];
-        float ps[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          float x0, x1;
-          add_f16x2_to_f32(s2[k], nb, x0, x1);   // exact score + nb, rounded once
-          const float e0 = ex2(x0), e1 = ex2(x1);
-          pk[k] = pack_f16(e0, e1);
-          ps[k & 3] += e0 + e1;
+          const float2 e = make_float2(ex2(sc[2 * k]), ex2(sc[2 * k + 1]));
+          pk[k] = pack_f16(e.x, e.y);
+          ps[k & 1] = add2(ps[k & 1], e);
         }
-        l_run = l_run * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+        l_run = l_run * alpha + ((ps[0].x + ps[0].y) + (ps[1].x + ps[1].y));
 
         if (__any_sync(0xffffffffu, move && j > 0)) {
           // rescaling O: the PV product of page gj - 1 (same item) must have landed

@@ -303,8 +303,10 @@ mla_status_t mla_kv_quantize_fp8(const void* kv, const int32_t* slots, int64_t n
  *   kv_pool_fp4  uint8 [num_blocks][64][416], 16-byte aligned (mla_kv_quantize_fp4 writes it)
  * Numerics: rows are widened on chip to fp16 (code * scale, rounded once), q_lat is rounded to
  * fp16, P is written as fp16, and the products accumulate in fp32; the RoPE
- * products are bf16, and partial scores are exchanged in fp16 as in
- * mla_decode_attn.  |q_lat| <= 65504 (else MLA_STATUS_SCORE_RANGE).  All other
+ * products are bf16.  The two halves of a row's columns (latent 0..255 with RoPE 0..31, and the
+ * rest) are scored apart: with partial scores p0, p1 in log2 units (logit / ln 2), each rounded to
+ * fp16 and added in fp32, a weight is off by a relative 2^-11 (|p0| + |p1|) ln 2 at worst.
+ * |q_lat| <= 65504 (else MLA_STATUS_SCORE_RANGE).  All other
  * arguments, outputs, status bits and the plan are those of mla_decode_attn;
  * mla_combine completes split rows.  No draft-tree masks.
  */
