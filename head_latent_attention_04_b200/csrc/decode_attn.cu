@@ -657,7 +657,7 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_consta
     const int tid = threadIdx.x - kSoftWarp0 * 32;    // 0 .. 255
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
     const uint32_t x_sendok_peer = mapa(smem_u32(&bars->x_sendok), peer);
-    bool out_of_range = false;   // a fp16 partial overflowed: a reference max of +Inf, or a NaN sum
+    bool out_of_range = false;   // fp16 partials overflowed: a reference max of +Inf or -Inf, or a NaN sum
     // The sequence length of the next item is loaded one item ahead, so that
     // the stale-plan check never waits for memory at an item boundary.
     // So is the next item's draft mask, when drafts form a tree.
@@ -831,7 +831,9 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_consta
         if (lane == 0) mbar_arrive(&bars->lsum[quarter]);
         if (!warp_wait(&bars->lsum[quarter], ii & 1, wc)) goto softmax_fail;
         l_run = ls[r] + ls[kRows + r];             // same order in both halves
-        out_of_range |= (m_ref == CUDART_INF_F) | (l_run != l_run);
+        // (every item attends a key, unless a draft mask hides them all, so no score above -Inf means that
+        // all of them left fp16 downwards)
+        out_of_range |= (m_ref == CUDART_INF_F) | (l_run != l_run) | (!kTree & !stale & (m_ref == -CUDART_INF_F));
         const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
         const bool valid = r < p.n_heads;
         const bool o_lat_32b = (reinterpret_cast<uintptr_t>(p.o_lat) & 31) == 0;

@@ -678,7 +678,7 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
     const int tid = threadIdx.x - kSoftWarp0 * 32;    // 0 .. 255
     const uint32_t lane_addr = (uint32_t)row0 << 16;
     const uint32_t x_sendok_peer = mapa(smem_u32(&bars->x_sendok), peer);
-    bool out_of_range = false;   // a fp16 partial overflowed: a reference max of +Inf, or a NaN sum
+    bool out_of_range = false;   // fp16 partials overflowed: a reference max of +Inf or -Inf, or a NaN sum
     // The sequence length of the next item is loaded one item ahead, so that
     // the stale-plan check never waits for memory at an item boundary.
     int T_next = it_begin < it_end ? p.seq_lens[items[(size_t)it_begin * kItemWords + kItB]] : 0;
@@ -829,7 +829,10 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
           const float other = __shfl_xor_sync(0xffffffffu, l_run, 16);
           l_run = c == 0 ? l_run + other : other + l_run;
         }
-        out_of_range |= (m_ref == CUDART_INF_F) | (l_run != l_run);
+        // (every item attends a key, so no score above -Inf means that all of them left fp16 downwards; a
+        // key here and there that does so has no weight either way, and looking for it in every
+        // page costs 2.3 %)
+        out_of_range |= (m_ref == CUDART_INF_F) | (l_run != l_run) | (!stale & (m_ref == -CUDART_INF_F));
         const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
         const bool valid = r < p.n_heads;
         const bool o_lat_32b = (reinterpret_cast<uintptr_t>(p.o_lat) & 31) == 0;

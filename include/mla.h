@@ -61,8 +61,11 @@ typedef enum {
 #define MLA_STATUS_BAD_SEQLEN  0x4   /* a row's device seq_lens disagrees with the plan: row skipped */
 #define MLA_STATUS_BAD_PLAN    0x8   /* the plan was made for other dims or another cluster count, or
                                         needs larger buffers than it was given: nothing computed */
-#define MLA_STATUS_SCORE_RANGE 0x10  /* a partial score of an attended key left the fp16 range
-                                        (|x| > 65504) or was not a number: outputs are invalid */
+#define MLA_STATUS_SCORE_RANGE 0x10  /* a partial score of an attended key was above the fp16 range
+                                        (65504) or not a number, or every attended key's was below
+                                        it: outputs are invalid.  (A key here and there whose partial
+                                        is below -65504 gets no weight; with draft masks a row of such
+                                        keys alone is written as one that sees no key) */
 #define MLA_STATUS_CACHE_RANGE 0x20  /* mla_kv_quantize_fp8: a 128-column block of c_KV has
                                         amax > 65504, beyond what mla_decode_attn_fp8cache widens
                                         (fp16); the row is written but must not be attended */

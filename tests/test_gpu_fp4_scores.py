@@ -133,3 +133,52 @@ def test_the_sum_of_the_halves_is_not_rounded(mla, big):
     got, lse, status = attend(mla, q, rows, scale)
     assert status == 0
     check(got, lse, q, rows, scale, exact_partials=True)
+
+
+@pytest.mark.parametrize("case", ["queries", "all keys", "one key", "up"])
+def test_partials_that_leave_fp16(mla, case):
+    """Above the range, or below it for every key: reported.  One key below it has no weight, as it should."""
+    T = 300
+    rows = np.zeros((T, 576))
+    rows[:, 0:512:32] = 6.0
+    q = np.zeros((4, 576))
+    q[:, 40] = 1.0
+    if case == "queries":
+        q[2, 0] = -2.0 ** 20                     # beyond fp16: -inf times 6 for every key
+    elif case == "all keys":
+        q[2, 0] = -2.0 ** 15                     # -196608 in log2 units
+    elif case == "one key":
+        rows[77, 33] = 6.0
+        q[2, 33] = -2.0 ** 15
+    else:
+        q[2, 0] = 2.0 ** 15
+    got, lse, status = attend(mla, q, rows, LN2)
+    assert status == (0 if case == "one key" else mla.STATUS_SCORE_RANGE)
+    if case == "one key":
+        check(got, lse, q, rows, LN2, exact_partials=True)
+    q[2, [0, 33]] = -2.0 ** 13                   # -49152: in range
+    got, lse, status = attend(mla, q, rows, LN2)
+    assert status == 0
+    check(got, lse, q, rows, LN2, exact_partials=True)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_other_caches_report_rows_below_fp16(mla, kind):
+    T, H = 200, 4
+    kv = torch.zeros((4, 64, 576), dtype=torch.bfloat16)
+    kv[..., 0] = 4.0
+    pool = kv.to(DEV) if kind == "bf16" else mla.fp8_pool_from(kv.to(DEV))
+    dims = mla.make_dims(1, 1, H, 4, 4, LN2)
+    plan, slots = mla.plan(dims, [T], 3)
+    plan = torch.from_numpy(plan).to(DEV)
+    o_part, lse_part = torch.empty(max(slots, 1) * H * 512, device=DEV), torch.empty(max(slots, 1) * H, device=DEV)
+    out, status = torch.empty((1, H, 512), dtype=torch.bfloat16, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    fn = mla.decode_attn if kind == "bf16" else mla.decode_attn_fp8cache
+    table = torch.arange(4, dtype=torch.int32, device=DEV)[None].contiguous()
+    lens = torch.tensor([T], dtype=torch.int32, device=DEV)
+    for size, want in ((-2.0 ** 12, 0), (-2.0 ** 15, mla.STATUS_SCORE_RANGE), (2.0 ** 15, mla.STATUS_SCORE_RANGE)):
+        q = torch.zeros((1, H, 512), dtype=torch.bfloat16, device=DEV)
+        q[0, 1, 0] = size
+        status.zero_()
+        fn(dims, q, q[..., 64:128].contiguous(), pool, table, lens, plan, 3, o_part, lse_part, out, status=status)
+        assert status.item() == want
