@@ -186,12 +186,13 @@ summarize_pages_kernel(const uint8_t* pool, const int32_t* blocks, int num_block
   if (amax > 0.0) {
     // rint(127 sum / amax) by a multiplication, good to 2^-44 absolute; closer than 2^-40 to
     // half-way the quotient itself decides
-    const double r = 127.0 / amax;
+    const double up = amax < 0x1p-900 ? 0x1p200 : 1.0;   // (sums below 2^-4: 127 / amax stays finite)
+    const double top = amax * up, r = 127.0 / top;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const double y = sum[i] * r;
+      const double x = sum[i] * up, y = x * r;
       q[i] = __double2int_rn(y);
-      if (fabs(fabs(y - (double)q[i]) - 0.5) < 0x1p-40) q[i] = __double2int_rn(sum[i] * 127.0 / amax);
+      if (fabs(fabs(y - (double)q[i]) - 0.5) < 0x1p-40) q[i] = __double2int_rn(x * 127.0 / top);
     }
   }
   reinterpret_cast<char2*>(codes + (size_t)blk * kDim)[threadIdx.x] = make_char2((signed char)q[0], (signed char)q[1]);
