@@ -42,8 +42,9 @@ __device__ __forceinline__ void report(int32_t* status, int bits) {
 // ---------------------------------------------------------------- summaries
 // One block per page: thread = (8 columns, 16 of the 64 rows), partial sums
 // joined through shared memory.  The floor is reading the page (8192 pages: bf16 92 us, FP8
-// 52, 4-bit 33 at the measured copy rate); it takes 106, 102 and 75 us, the smaller rows
-// because what a value costs after it is read weighs more.  So the widening to fp64 is done
+// 52, 4-bit 33 at the measured copy rate); it takes 107, 109 and 75 us (106, 102 and 75
+// without looking for Inf and NaN), the smaller rows because what a value costs after it is read
+// weighs more.  So the widening to fp64 is done
 // on the bits: the exponent and mantissa of a bf16, fp16 or E2M1 value placed in a
 // double's fields without correcting the bias read as the value times a power of two,
 // subnormals included (all kinds end in units of 2^896), and the 4-bit rows are summed in
@@ -57,14 +58,34 @@ constexpr int kF8Row = 656, kF8ScaleOff = 512, kF8RopeOff = 528;
 
 __device__ __forceinline__ double from_hi(uint32_t hi) { return __hiloint2double((int)hi, 0); }
 
-// acc[i] += 2^-896 x (bf16 value i of the 16 bytes)
-__device__ __forceinline__ void add_bf16x8(const uint4& v, double (&acc)[8]) {
+// acc[i] += 2^-896 x (bf16 value i of the 16 bytes).  An Inf or a NaN is seen in `special` (not_finite): as
+// the largest magnitudes of the pairs of values, their signs meaningless, NaN above all (kMax: one
+// instruction a pair, but one chain), or as bits 15 and 31, into which an exponent of all ones
+// carries (short chains, which the one warp that reads k_rope alone needs).
+template <bool kMax>
+__device__ __forceinline__ void add_bf16x8(const uint4& v, double (&acc)[8], uint32_t& special) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t carry[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    if (kMax) asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(special) : "r"(w[i]));
+    else carry[i] = (w[i] & 0x7F807F80u) + 0x00800080u;
     acc[2 * i] += from_hi(((w[i] << 16) & 0x80000000u) | ((w[i] & 0x7FFFu) << 13));
     acc[2 * i + 1] += from_hi((w[i] & 0x80000000u) | ((w[i] & 0x7FFF0000u) >> 3));
   }
+  if (!kMax) special |= (carry[0] | carry[1]) | (carry[2] | carry[3]);
+}
+template <bool kMax>
+__device__ __forceinline__ bool not_finite(uint32_t special) {
+  return kMax ? max(special & 0x7FFFu, (special >> 16) & 0x7FFFu) >= 0x7F80u : (special & 0x80008000u) != 0;
+}
+
+// Four E4M3 codes (byte i = code i) -> two fp16 pairs, exact (NaN codes become 0x7FFF).
+__device__ __forceinline__ void cvt_e4m3x4_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 c01, c23;\n\tmov.b32 {c01, c23}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, c01;\n\tcvt.rn.f16x2.e4m3x2 %1, c23;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
 }
 
 template <Cache kind>
@@ -88,25 +109,33 @@ summarize_pages_kernel(const uint8_t* pool, const int32_t* blocks, int num_block
   const int c = t < 256 ? t % 64 : 64 + t % 8, part = t < 256 ? t / 64 : (t - 256) / 8;
   const uint8_t* row = pool + ((size_t)blk * kPage + part * kRows) * kRowBytes;
   double acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  bool finite = true;   // what this thread read
   if (kind == Cache::kBf16 || c >= 64) {
     const uint8_t* src = kind == Cache::kBf16 ? row + 16 * c : row + kRope + 16 * (c - 64);
+    uint32_t special = 0;
 #pragma unroll 8
-    for (int r = 0; r < kRows; ++r) add_bf16x8(__ldcg(reinterpret_cast<const uint4*>(src + r * kRowBytes)), acc);
+    for (int r = 0; r < kRows; ++r)
+      add_bf16x8<kind == Cache::kBf16>(__ldcg(reinterpret_cast<const uint4*>(src + r * kRowBytes)), acc, special);
+    finite = !not_finite<kind == Cache::kBf16>(special);
   } else if (kind == Cache::kFp8) {
+    uint32_t nan_codes = 0;   // bit 7 of a byte: a code was 0x7F or 0xFF
 #pragma unroll 8
     for (int r = 0; r < kRows; ++r) {
       const uint2 v = __ldcg(reinterpret_cast<const uint2*>(row + r * kRowBytes) + c);
       const float s = __ldcg(reinterpret_cast<const float*>(row + r * kRowBytes + kF8ScaleOff) + (c >> 4));
       const double sd = (double)s * 0x1p112;
+      nan_codes |= ((v.x & 0x7F7F7F7Fu) + 0x01010101u) | ((v.y & 0x7F7F7F7Fu) + 0x01010101u);
       uint32_t h[4];
-      dequant_e4m3x4_f16(v.x, 0x3C003C00u, h[0], h[1]);   // codes as fp16 (times 1), exact
-      dequant_e4m3x4_f16(v.y, 0x3C003C00u, h[2], h[3]);
+      cvt_e4m3x4_f16(v.x, h[0], h[1]);
+      cvt_e4m3x4_f16(v.y, h[2], h[3]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         acc[2 * i] += sd * from_hi(((h[i] << 16) & 0x80000000u) | ((h[i] & 0x7FFFu) << 10));
         acc[2 * i + 1] += sd * from_hi((h[i] & 0x80000000u) | ((h[i] & 0x7FFF0000u) >> 6));
       }
     }
+    // (a scale that is not finite makes every sum so: 0 times it is NaN)
+    finite = fabs(acc[0]) < CUDART_INF && (nan_codes & 0x80808080u) == 0;
   } else {
     const uint32_t* src = reinterpret_cast<const uint32_t*>(row) + c;
     uint32_t h[kRows], top = 0, low = 31;   // the rows' fp16 scales, their largest and smallest exponent
@@ -148,6 +177,7 @@ summarize_pages_kernel(const uint8_t* pool, const int32_t* blocks, int num_block
         const uint32_t scale = __ldcg(reinterpret_cast<const uint16_t*>(row + r * kRowBytes + kF4ScaleOff) + (c >> 2));
         // fp16 scale x 2^-1008, then x 2^1134: times the codes' 2^-1022 the product is in units of 2^896
         const double sd = from_hi((scale & 0x7FFFu) << 10) * 0x1p1000 * 0x1p134;
+        finite &= (scale & 0x7C00u) != 0x7C00u;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint32_t sign = (i == 7 ? codes8 : codes8 << (28 - 4 * i)) & 0x80000000u;
@@ -176,14 +206,16 @@ summarize_pages_kernel(const uint8_t* pool, const int32_t* blocks, int num_block
   const double big = fabs(sum[0]) > fabs(sum[1]) ? fabs(sum[0]) : fabs(sum[1]);
   const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)__double2hiint(big));
   const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)__double2hiint(big) == hi ? (uint32_t)__double2loint(big) : 0u);
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x / 32] = (unsigned long long)hi << 32 | lo;
+  const bool warp_finite = __all_sync(0xffffffffu, finite);
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x / 32] = warp_finite ? (unsigned long long)hi << 32 | lo : ~0ull;
   __syncthreads();
   unsigned long long m = s_max[0];
 #pragma unroll
   for (int i = 1; i < kSumThreads / 32; ++i) m = max(m, s_max[i]);
+  const bool usable = m != ~0ull;   // no Inf or NaN in the page
   const double amax = __longlong_as_double((long long)m);
   int q[2] = {0, 0};
-  if (amax > 0.0) {
+  if (amax > 0.0 && usable) {
     // rint(127 sum / amax) by a multiplication, good to 2^-44 absolute; closer than 2^-40 to
     // half-way the quotient itself decides
     const double up = amax < 0x1p-900 ? 0x1p200 : 1.0;   // (sums below 2^-4: 127 / amax stays finite)
@@ -196,7 +228,10 @@ summarize_pages_kernel(const uint8_t* pool, const int32_t* blocks, int num_block
     }
   }
   reinterpret_cast<char2*>(codes + (size_t)blk * kDim)[threadIdx.x] = make_char2((signed char)q[0], (signed char)q[1]);
-  if (threadIdx.x == 0) scales[blk] = (float)(amax * 0x1p890 / 127.0);   // 2^896 / 64
+  if (threadIdx.x == 0) {
+    scales[blk] = usable ? (float)(amax * 0x1p890 / 127.0) : CUDART_NAN_F;   // 2^896 / 64
+    if (!usable) report(status, MLA_STATUS_CACHE_RANGE);
+  }
 }
 
 // ---------------------------------------------------------------- scores

@@ -68,7 +68,9 @@ typedef enum {
                                         keys alone is written as one that sees no key) */
 #define MLA_STATUS_CACHE_RANGE 0x20  /* mla_kv_quantize_fp8: a 128-column block of c_KV has
                                         amax > 65504, beyond what mla_decode_attn_fp8cache widens
-                                        (fp16); the row is written but must not be attended */
+                                        (fp16); the row is written but must not be attended.
+                                        mla_kv_quantize_fp4: the same of a 32-column group.
+                                        mla_summarize_pages: a page holds an Inf or a NaN */
 
 #define MLA_STATUS_NO_SPACE    0x40  /* mla_build_tables: a request got no new tokens (no free block, longer
                                         than its table row, no room in the slot map, or a bad length) */
@@ -415,8 +417,8 @@ mla_status_t mla_plan_device(const mla_dims_t* dims, const int32_t* seq_lens, in
  * page's 64 rows [c_KV | k_rope], scale = amax / 127, code = rint(127 m / amax)
  * (0 and 0 when amax = 0).  Call it when a page fills; a page that still grows needs none (it
  * is among the recent pages).
- *   kv_pool   the pool, of kind `cache` (MLA_CACHE_BF16, _FP8 or _FP4); the pages' values must be
- *             finite (a summary of others holds no meaning, and is not reported)
+ *   kv_pool   the pool, of kind `cache` (MLA_CACHE_BF16, _FP8 or _FP4).  A page that holds an Inf or a
+ *             NaN is reported (MLA_STATUS_CACHE_RANGE) and gets codes 0 and a scale of NaN
  *   blocks    int32 [n]  pages to summarise; -1 is skipped, others outside the pool are reported
  *             (MLA_STATUS_BAD_BLOCK) and skipped
  *   codes     int8 [num_blocks][576], 16-byte aligned, and scales fp32 [num_blocks]: the entries of
@@ -440,7 +442,8 @@ mla_status_t mla_plan_device(const mla_dims_t* dims, const int32_t* seq_lens, in
  *             (mla_plan_size with B = N, s_q = 1, max_blocks_per_seq = k; dims->causal = 1), made
  *             beside the selection.  num_clusters and plan_bytes count only with it
  *   status    MLA_STATUS_BAD_SEQLEN: a length below s_q or beyond the table (the row selects nothing);
- *             MLA_STATUS_BAD_BLOCK: a scored page's block lies outside the pool (scored -inf)
+ *             MLA_STATUS_BAD_BLOCK: a scored page's block lies outside the pool (scored -inf).  A page
+ *             whose scale is NaN or negative is scored -inf too
  * The attention then takes dims with B = N, s_q = 1, causal = 1 and
  * max_blocks_per_seq = k, sel_table, sel_lens and that plan.  Queries must be finite.
  */
