@@ -38,6 +38,16 @@ __device__ __forceinline__ void report(int32_t* status, int bits) {
   if (status) atomicOr(status, bits);
 }
 
+// fma(x, r, 48) - 48 of a pair, each step rounded to nearest.
+__device__ __forceinline__ float2 to_grid(float2 x, float r) {
+  float2 y;
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %5};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 c, {%6, %6};\n\tadd.rn.f32x2 a, a, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(x.x), "f"(x.y), "f"(r), "f"(48.f), "f"(-48.f));
+  return y;
+}
+
 // One thread's part of a row: 8 columns of c_KV, or 16 bytes of k_rope (c >= kLatChunks).
 // `live` is the same for the four threads of a group.
 __device__ __forceinline__ void quantize_chunk(uint4 v, int c, bool live, uint8_t* dst, int32_t* status) {
@@ -68,14 +78,15 @@ __device__ __forceinline__ void quantize_chunk(uint4 v, int c, bool live, uint8_
   const float r = s > 0.f ? 1.f / s : 0.f;
   // x r is within 2^-22 of x / s (relative).  A quotient that is not half-way
   // between two grid values is at least 2^-13 away from it (x has 8 significant bits,
-  // s 11, a half-way point 3), and |x / s| < 8.5 unless the row is flagged, so
-  // adding and taking off 48 (a grid of 2^-18) moves only the exact ties, onto the
-  // tie: the codes are those of the exact quotient.
+  // s 11, a half-way point 3), and |x / s| <= 9 unless the row is flagged (a subnormal s may be two
+  // thirds of amax / 6), so adding and taking off 48 (a grid of 2^-18) moves only the exact ties, onto the
+  // tie: the codes are those of the exact quotient.  The sum loses the sign of what becomes 0: a
+  // code keeps the sign of its value (8 is -0).
   uint32_t codes = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float y0 = __fsub_rn(__fmaf_rn(x[2 * i], r, 48.f), 48.f), y1 = __fsub_rn(__fmaf_rn(x[2 * i + 1], r, 48.f), 48.f);
-    codes |= cvt_e2m1x2(y0, y1) << (8 * i);
+    const float2 y = to_grid(make_float2(x[2 * i], x[2 * i + 1]), r);
+    codes |= cvt_e2m1x2(copysignf(y.x, x[2 * i]), copysignf(y.y, x[2 * i + 1])) << (8 * i);
   }
   reinterpret_cast<uint32_t*>(dst)[c] = codes;
   if ((c & 3) == 0) {

@@ -324,7 +324,7 @@ mla_status_t mla_decode_attn_fp4cache(const mla_dims_t* dims, const void* q_lat,
 /*
  * mla_kv_quantize_fp4 -- write cache rows into 4-bit pool slots.  Per group of 32
  * columns: s = fp16(max |x| / 6), code = E2M1(x / s) rounded to nearest even
- * and saturated at 6 (s = 0: all codes 0); k_rope is copied.
+ * and saturated at 6, with the sign of x (8 is -0; s = 0: 0 or 8); k_rope is copied.
  *   kv        bf16 [n][576]  rows c_KV (512) | k_rope (64), 16-byte aligned
  *   slots     int32 [n]      destination of row i: block * 64 + row in the block; -1: padding, the
  *             row is skipped (the slot maps of mla_build_tables end in them)
