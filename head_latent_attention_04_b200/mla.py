@@ -164,12 +164,13 @@ def _on(*tensors):
     return _SAME_DEVICE if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
-def _made_on(stream):
+def _made_on(stream, device):
     """Context in which a call's own tensors are made: on the stream that the call
-    uses, so that their memory and their fills belong to it."""
+    uses, so that their memory and their fills belong to it.  A raw handle is taken
+    for a stream of the tensors' device, whichever is current."""
     if stream is None:
         return _SAME_DEVICE
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device))
 
 
 def _stream(stream=None) -> int:
@@ -400,7 +401,7 @@ def kv_dequantize_fp4(kv_pool_fp4, slots, kv=None, status=None, stream=None):
     bad slots are left as they were; zeros when ``kv`` is made here)."""
     nb, n = kv_pool_fp4.shape[0], slots.shape[0]
     if kv is None:
-        with _made_on(stream):
+        with _made_on(stream, kv_pool_fp4.device):
             kv = torch.zeros((n, 576), dtype=torch.bfloat16, device=kv_pool_fp4.device)
     with _on(kv_pool_fp4, kv, slots, status):
         _check(_lib.mla_kv_dequantize_fp4(_arg(kv_pool_fp4, "kv_pool_fp4", torch.uint8, nb, 64, FP4_ROW_BYTES),
@@ -413,7 +414,7 @@ def kv_dequantize_fp4(kv_pool_fp4, slots, kv=None, status=None, stream=None):
 def fp4_pool_from(kv_pool, stream=None):
     """The 4-bit copy of a whole bf16 pool [num_blocks][64][576] (every slot quantised)."""
     nb = kv_pool.shape[0]
-    with _made_on(stream):
+    with _made_on(stream, kv_pool.device):
         pool4 = torch.empty((nb, 64, FP4_ROW_BYTES), dtype=torch.uint8, device=kv_pool.device)
         slots = torch.arange(nb * 64, dtype=torch.int32, device=kv_pool.device)
     return kv_quantize_fp4(kv_pool.reshape(nb * 64, 576), slots, pool4, stream=stream)
@@ -453,7 +454,7 @@ def build_tables(cached_lens, new_lens, block_table, free_blocks, free_head, max
     B, width = cached_lens.shape[0], block_table.shape[-1]
     i32 = torch.int32
     if out is None:
-        with _made_on(stream):
+        with _made_on(stream, block_table.device):
             out = BatchTables.empty(B, max_new, block_table.device)
         at = out.seq_lens.data_ptr()              # the five arrays of empty(), one behind the other
         lens, cu, slots, positions = at, at + 4 * B, at + 8 * B + 4, at + 8 * B + 4 + 4 * max_new
@@ -483,7 +484,7 @@ def plan_device(dims: MlaDims, seq_lens, num_clusters: int, plan_dev=None, statu
     """:func:`plan` made on the GPU from device ``seq_lens`` (int32 [B]; 0 is a
     padded row without work): the same words, as an int32 device tensor."""
     if plan_dev is None:
-        with _made_on(stream):
+        with _made_on(stream, seq_lens.device):
             plan_dev = torch.empty(_plan_words(dims.B * dims.s_q, num_clusters), dtype=torch.int32, device=seq_lens.device)
     with _on(seq_lens, plan_dev, status):
         _check(_lib.mla_plan_device(ctypes.byref(dims), _arg(seq_lens, "seq_lens", torch.int32, dims.B), num_clusters,

@@ -53,3 +53,18 @@ def test_subnormal_scales(mla, exponent):
     g = torch.Generator().manual_seed(-exponent)
     kv = (torch.randn((200, 576), generator=g) * 2.0 ** exponent * 8).to(torch.bfloat16)
     np.testing.assert_array_equal(written(mla, kv), pack_rows(kv))
+
+
+def test_raw_stream_handles(mla):
+    """A call given a stream as a number makes its own tensors on that stream too."""
+    kv = rows_of_many_ranges(500, 5).to(DEV)
+    pool = torch.zeros((8, 64, 416), dtype=torch.uint8, device=DEV)
+    slots = torch.arange(500, dtype=torch.int32, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    mla.kv_quantize_fp4(kv, slots, pool, stream=side.cuda_stream)
+    back = mla.kv_dequantize_fp4(pool, slots, stream=side.cuda_stream)
+    side.synchronize()
+    want = mla.kv_dequantize_fp4(pool, slots)
+    torch.cuda.synchronize()
+    assert torch.equal(back, want)
