@@ -529,6 +529,7 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_consta
       const int32_t* w = items + (size_t)it * kItemWords;
       const int ii = it - it_begin;
       if (ii > 0 && !warp_wait(&bars->q_empty, (ii - 1) & 1, wc)) goto sender_fail;
+      tc_fence_after();   // q_lat is written after the last item's products have read it
       {
         {
           const uint4* rsrc = reinterpret_cast<const uint4*>(p.q_rope + ((size_t)w[kItRow] * p.n_heads + r) * 64 +
@@ -797,6 +798,7 @@ mla_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_consta
 
         // P buffer gj & 1 is free once the PV product of page gj - 2 has completed
         if (gj >= 2 && !warp_wait(&bars->o_full[gj & 1], ((gj >> 1) - 1) & 1, wc)) goto softmax_fail;
+        tc_fence_after();   // P is written after the product that read this buffer
         if (__any_sync(0xffffffffu, move && j > 0)) {
           // rescaling O: the PV product of page gj - 1 (same item) must have landed
           if (!warp_wait(&bars->o_full[(gj - 1) & 1], ((gj - 1) >> 1) & 1, wc)) goto softmax_fail;

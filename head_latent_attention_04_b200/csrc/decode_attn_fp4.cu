@@ -560,6 +560,7 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
       const int32_t* w = items + (size_t)it * kItemWords;
       const int ii = it - it_begin;
       if (ii > 0 && !warp_wait(&bars->q_empty, (ii - 1) & 1, wc)) goto sender_fail;
+      tc_fence_after();   // q_lat is written after the last item's products have read it
       {
         if (half == 0) {
           const uint4* rsrc = reinterpret_cast<const uint4*>(p.q_rope + ((size_t)w[kItRow] * p.n_heads + r) * 64 +
@@ -813,6 +814,7 @@ mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid
           }
           tmem_st_wait();
         }
+        tc_fence_after();   // after the product that read this buffer (awaited above)
         tmem_st16x2_16<16>(tmem + lane_addr + kTmemP + 32 * (gj & 1), pk);   // keys [32c, 32c+32), fp16 pairs
         tmem_st_wait();
         tc_fence_before();

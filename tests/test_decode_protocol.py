@@ -201,3 +201,21 @@ def test_the_peer_tile_is_read_before_it_is_refilled(kernel):
     assert text.count("mbar_arrive_relaxed_cluster(") == text.count("mbar_arrive_relaxed_cluster(ok_addr)") == 1
     assert text.count("mbar_wait<true, kWaitHintNs>(&bars->x_sendok") == 1
     assert "mbar_wait<false, kWaitHintNs>(&bars->x_sendok" not in text
+
+
+@pytest.mark.parametrize("kernel", ["decode_attn", "decode_attn_fp4"])
+def test_tensor_memory_is_written_behind_a_fence(kernel):
+    """A wait for the products that read a tensor-memory operand orders this thread's next stores into it
+    only together with tcgen05.fence::after_thread_sync."""
+    text = " ".join(re.sub(r"//.*", "", source(kernel)).split())
+    q = text.split("warp_wait(&bars->q_empty, (ii - 1) & 1, wc)) goto sender_fail;")[1]
+    assert "tc_fence_after();" in q[:q.index("tmem_st32(")]
+    p = text.split("warp_wait(&bars->o_full[gj & 1], ((gj >> 1) - 1) & 1, wc)) goto softmax_fail;")[1]
+    p = p[:p.index("tmem + lane_addr + kTmemP")]
+    rescale = p[p.index("if (__any_sync(0xffffffffu, move && j > 0)) {"):]
+    depth, end = 0, 0
+    for end, ch in enumerate(rescale):                       # the block that rescales O has a fence of its own
+        depth += (ch == "{") - (ch == "}")
+        if ch == "}" and depth == 0:
+            break
+    assert "tc_fence_after();" in p.replace(rescale[:end + 1], "")
