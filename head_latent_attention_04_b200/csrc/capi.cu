@@ -500,27 +500,28 @@ mla_status_t mla_combine(const mla_dims_t* dims, const void* plan_dev, const flo
 
 // Pointers and workspaces of the two entry points that are given the buffers' sizes.
 static mla_status_t check_sized(const mla_dims_t& d, const void* plan_dev, size_t plan_bytes, int32_t num_clusters,
-                                const float* o_part, const float* lse_part, int32_t part_slots, PlanRoom* room) {
+                                const float* o_part, size_t o_part_bytes, const float* lse_part,
+                                size_t lse_part_bytes, PlanRoom* room) {
   MLA_TRY(check_words(plan_dev, "plan_dev"));
-  if (part_slots < 0) return set_error(MLA_ERR_INVALID_ARG, "part_slots must be >= 0");
-  if (part_slots > 0) {
-    if (!o_part || !lse_part) return set_error(MLA_ERR_INVALID_ARG, "part_slots > 0 needs o_part and lse_part");
-    if ((reinterpret_cast<uintptr_t>(o_part) & 31u) || (reinterpret_cast<uintptr_t>(lse_part) & 3u))
-      return set_error(MLA_ERR_INVALID_ARG, "o_part must be 32-byte aligned, lse_part 4-byte aligned");
-  }
+  if ((o_part_bytes && !o_part) || (lse_part_bytes && !lse_part))
+    return set_error(MLA_ERR_INVALID_ARG, "o_part / lse_part is NULL");
+  if ((reinterpret_cast<uintptr_t>(o_part) & 31u) || (reinterpret_cast<uintptr_t>(lse_part) & 3u))
+    return set_error(MLA_ERR_INVALID_ARG, "o_part must be 32-byte aligned, lse_part 4-byte aligned");
   // header, cluster ranges and row section: what is read before the plan's own size is known
   if (plan_bytes / 4 < (size_t)(kPlanHeaderWords + num_clusters + 1) + (size_t)d.B * d.s_q + 1)
     return set_error(MLA_ERR_WORKSPACE_TOO_SMALL, "plan_bytes is less than any plan of these dims");
-  const size_t words = plan_bytes / 4;
-  *room = {words > INT32_MAX ? INT32_MAX : (int)words, part_slots};
+  const size_t head = (size_t)d.n_heads * 4, words = plan_bytes / 4;
+  const size_t by_o = o_part_bytes / (512 * head), by_lse = lse_part_bytes / head;
+  const size_t slots = by_o < by_lse ? by_o : by_lse;
+  *room = {words > INT32_MAX ? INT32_MAX : (int)words, slots > INT32_MAX ? INT32_MAX : (int)slots};
   return MLA_OK;
 }
 
 mla_status_t mla_decode_attn_sized(const mla_dims_t* dims, int32_t cache, const void* q_lat, const void* q_rope,
                                    const void* kv_pool, const int32_t* block_table, const int32_t* seq_lens,
                                    const int32_t* draft_masks, const void* plan_dev, size_t plan_bytes,
-                                   int32_t num_clusters, float* o_part, float* lse_part, int32_t part_slots,
-                                   void* o_lat, float* lse_out, int32_t* status, void* stream) {
+                                   int32_t num_clusters, float* o_part, size_t o_part_bytes, float* lse_part,
+                                   size_t lse_part_bytes, void* o_lat, float* lse_out, int32_t* status, void* stream) {
   clear_error();
   MLA_TRY(check_dims(dims));
   if (cache != MLA_CACHE_BF16 && cache != MLA_CACHE_FP8 && cache != MLA_CACHE_FP4)
@@ -540,7 +541,7 @@ mla_status_t mla_decode_attn_sized(const mla_dims_t* dims, int32_t cache, const 
   MLA_TRY(check_optional_words(lse_out, "lse_out"));
   MLA_TRY(check_optional_words(status, "status"));
   PlanRoom room;
-  MLA_TRY(check_sized(*dims, plan_dev, plan_bytes, num_clusters, o_part, lse_part, part_slots, &room));
+  MLA_TRY(check_sized(*dims, plan_dev, plan_bytes, num_clusters, o_part, o_part_bytes, lse_part, lse_part_bytes, &room));
   const int32_t* plan = static_cast<const int32_t*>(plan_dev);
   if (cache == MLA_CACHE_BF16)
     return launch_decode_attn(*dims, q_lat, q_rope, kv_pool, block_table, seq_lens, draft_masks, plan, num_clusters,
@@ -551,8 +552,8 @@ mla_status_t mla_decode_attn_sized(const mla_dims_t* dims, int32_t cache, const 
 }
 
 mla_status_t mla_combine_sized(const mla_dims_t* dims, const void* plan_dev, size_t plan_bytes, const float* o_part,
-                               const float* lse_part, int32_t part_slots, void* o_lat, float* lse_out,
-                               int32_t* status, void* stream) {
+                               size_t o_part_bytes, const float* lse_part, size_t lse_part_bytes, void* o_lat,
+                               float* lse_out, int32_t* status, void* stream) {
   clear_error();
   MLA_TRY(check_dims(dims));
   MLA_TRY(check_ptr(o_lat, "o_lat"));
@@ -560,7 +561,7 @@ mla_status_t mla_combine_sized(const mla_dims_t* dims, const void* plan_dev, siz
   MLA_TRY(check_optional_words(status, "status"));
   if (!o_part || !lse_part) return set_error(MLA_ERR_INVALID_ARG, "o_part / lse_part is NULL");
   PlanRoom room;
-  MLA_TRY(check_sized(*dims, plan_dev, plan_bytes, 1, o_part, lse_part, part_slots, &room));
+  MLA_TRY(check_sized(*dims, plan_dev, plan_bytes, 1, o_part, o_part_bytes, lse_part, lse_part_bytes, &room));
   return launch_combine(*dims, static_cast<const int32_t*>(plan_dev), dims->B * dims->s_q, o_part, lse_part, room,
                         o_lat, lse_out, status, stream);
 }

@@ -61,9 +61,9 @@ for _name, _args in {
     "mla_decode_attn_tree": [_pdims, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp],
     "mla_decode_attn_fp8cache": [_pdims, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp],
     "mla_kv_quantize_fp8": [_vp, _vp, ctypes.c_int64, _vp, _i32, _vp, _vp],
-    "mla_decode_attn_sized": [_pdims, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i32, _vp, _vp, _i32, _vp, _vp, _vp,
+    "mla_decode_attn_sized": [_pdims, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i32, _vp, _sz, _vp, _sz, _vp, _vp, _vp,
                               _vp],
-    "mla_combine_sized": [_pdims, _vp, _sz, _vp, _vp, _i32, _vp, _vp, _vp, _vp],
+    "mla_combine_sized": [_pdims, _vp, _sz, _vp, _sz, _vp, _sz, _vp, _vp, _vp, _vp],
     "mla_kv_quantize_fp4": [_vp, _vp, ctypes.c_int64, _vp, _i32, _vp, _vp],
     "mla_kv_dequantize_fp4": [_vp, _vp, ctypes.c_int64, _vp, _i32, _vp, _vp],
     "mla_decode_attn_fp4cache": [_pdims, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp],
@@ -114,18 +114,24 @@ def _ptr(t) -> int | None:
     (read as if contiguous) is refused here, before anything is launched."""
     if t is None:
         return None
-    if isinstance(t, int):
-        return t
+    try:
+        if t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        if isinstance(t, int):
+            return t
+        raise
     if not t.is_cuda:
         raise ValueError(f"expected a CUDA tensor, got one on {t.device}")
-    if not t.is_contiguous():
-        raise ValueError("expected a contiguous tensor (the library assumes row-major layouts)")
-    return t.data_ptr()
+    raise ValueError("expected a contiguous tensor (the library assumes row-major layouts)")
 
 
 # The step's calls are launch-bound at decode sizes, so the checks of a call that
 # is right take a few attribute reads per tensor; the messages are made only for
 # one that is wrong.
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
 def _arg(t, name: str, dtype, *shape) -> int | None:
     """Device address of a tensor argument of the given type and shape, refused
     here when it is anything else (its device is checked by _on)."""
@@ -295,29 +301,24 @@ def out_uv_fp8(o_lat: torch.Tensor, w: Fp8Weight, out: torch.Tensor | None = Non
     return out
 
 
-def _room(dims, num_clusters, plan_dev, o_part, lse_part):
-    """(bytes of the plan's buffer, partial slots that both workspaces hold): the kernels
-    refuse a plan that needs more (STATUS_BAD_PLAN).  Raw addresses are taken to
-    have plan_size's sizes."""
-    H, N = dims.n_heads, dims.B * dims.s_q
-    if isinstance(plan_dev, int):
-        plan_bytes = 4 * _plan_words(N, num_clusters)
-    else:
-        plan_bytes = 0 if plan_dev is None else plan_dev.numel() * plan_dev.element_size()
-    if o_part is None or lse_part is None:
-        return plan_bytes, 0
-    bound = num_clusters + N
-    return plan_bytes, min(bound if isinstance(o_part, int) else o_part.numel() // (H * 512),
-                           bound if isinstance(lse_part, int) else lse_part.numel() // H)
+def _sizes(dims, num_clusters, plan_dev, o_part, lse_part):
+    """Bytes of a plan's buffer and of the workspaces: the kernels refuse a plan that
+    needs more (STATUS_BAD_PLAN).  Raw addresses are taken to have plan_size's sizes."""
+    try:
+        return plan_dev.nbytes, o_part.nbytes, lse_part.nbytes
+    except AttributeError:          # None or an address among them
+        bound = plan_size(dims, num_clusters)
+        return tuple(0 if t is None else b if isinstance(t, int) else t.nbytes
+                     for t, b in zip((plan_dev, o_part, lse_part), bound))
 
 
 def _decode_attn(what, cache, dims, q_lat, q_rope, kv_pool, block_table, seq_lens, draft_masks, plan_dev, num_clusters,
                  o_part, lse_part, o_lat, lse_out, status, stream):
-    plan_bytes, slots = _room(dims, num_clusters, plan_dev, o_part, lse_part)
+    plan_bytes, o_bytes, lse_bytes = _sizes(dims, num_clusters, plan_dev, o_part, lse_part)
     _check(_lib.mla_decode_attn_sized(ctypes.byref(dims), CACHE_KINDS[cache], _ptr(q_lat), _ptr(q_rope), _ptr(kv_pool),
                                       _ptr(block_table), _ptr(seq_lens), _ptr(draft_masks), _ptr(plan_dev), plan_bytes,
-                                      num_clusters, _ptr(o_part), _ptr(lse_part), slots, _ptr(o_lat), _ptr(lse_out),
-                                      _ptr(status), _stream(stream)), what)
+                                      num_clusters, _ptr(o_part), o_bytes, _ptr(lse_part), lse_bytes, _ptr(o_lat),
+                                      _ptr(lse_out), _ptr(status), _stream(stream)), what)
 
 
 def decode_attn(dims, q_lat, q_rope, kv_pool, block_table, seq_lens, plan_dev, num_clusters,
@@ -373,16 +374,16 @@ def decode_attn_fp4cache(dims, q_lat, q_rope, kv_pool_fp4, block_table, seq_lens
     [num_blocks][64][416] as :func:`kv_quantize_fp4` writes it."""
     N, H = dims.B * dims.s_q, dims.n_heads
     with _on(q_lat, q_rope, kv_pool_fp4, block_table, seq_lens, plan_dev, o_part, lse_part, o_lat, lse_out, status):
-        plan_bytes, slots = _room(dims, num_clusters, plan_dev, o_part, lse_part)
         _check(_lib.mla_decode_attn_sized(
-            ctypes.byref(dims), CACHE_KINDS["fp4"], _arg(q_lat, "q_lat", torch.bfloat16, N, H, 512),
-            _arg(q_rope, "q_rope", torch.bfloat16, N, H, 64),
-            _arg(kv_pool_fp4, "kv_pool_fp4", torch.uint8, dims.num_blocks, 64, FP4_ROW_BYTES),
-            _arg(block_table, "block_table", torch.int32, dims.B, dims.max_blocks_per_seq),
-            _arg(seq_lens, "seq_lens", torch.int32, dims.B), None, _vec(plan_dev, "plan_dev", torch.int32), plan_bytes,
-            num_clusters, _vec(o_part, "o_part", torch.float32), _vec(lse_part, "lse_part", torch.float32), slots,
-            _arg(o_lat, "o_lat", torch.bfloat16, N, H, 512), _arg(lse_out, "lse_out", torch.float32, N, H),
-            _vec(status, "status", torch.int32), _stream(stream)), "mla_decode_attn_fp4cache")
+            ctypes.byref(dims), CACHE_KINDS["fp4"], _arg(q_lat, "q_lat", _BF16, N, H, 512),
+            _arg(q_rope, "q_rope", _BF16, N, H, 64),
+            _arg(kv_pool_fp4, "kv_pool_fp4", _U8, dims.num_blocks, 64, FP4_ROW_BYTES),
+            _arg(block_table, "block_table", _I32, dims.B, dims.max_blocks_per_seq),
+            _arg(seq_lens, "seq_lens", _I32, dims.B), None, _vec(plan_dev, "plan_dev", _I32),
+            0 if plan_dev is None else plan_dev.nbytes, num_clusters, _vec(o_part, "o_part", _F32),
+            0 if o_part is None else o_part.nbytes, _vec(lse_part, "lse_part", _F32),
+            0 if lse_part is None else lse_part.nbytes, _arg(o_lat, "o_lat", _BF16, N, H, 512), _arg(lse_out, "lse_out", _F32, N, H),
+            _vec(status, "status", _I32), _stream(stream)), "mla_decode_attn_fp4cache")
 
 
 def kv_quantize_fp4(kv, slots, kv_pool_fp4, status=None, stream=None):
@@ -390,9 +391,9 @@ def kv_quantize_fp4(kv, slots, kv_pool_fp4, status=None, stream=None):
     row; -1 is padding) of the 4-bit pool (uint8 [num_blocks][64][416])."""
     nb, n = kv_pool_fp4.shape[0], slots.shape[0]
     with _on(kv_pool_fp4, kv, slots, status):
-        _check(_lib.mla_kv_quantize_fp4(_arg(kv, "kv", torch.bfloat16, n, 576), _arg(slots, "slots", torch.int32, n), n,
-                                        _arg(kv_pool_fp4, "kv_pool_fp4", torch.uint8, nb, 64, FP4_ROW_BYTES),
-                                        nb, _vec(status, "status", torch.int32), _stream(stream)), "mla_kv_quantize_fp4")
+        _check(_lib.mla_kv_quantize_fp4(_arg(kv, "kv", _BF16, n, 576), _arg(slots, "slots", _I32, n), n,
+                                        _arg(kv_pool_fp4, "kv_pool_fp4", _U8, nb, 64, FP4_ROW_BYTES),
+                                        nb, _vec(status, "status", _I32), _stream(stream)), "mla_kv_quantize_fp4")
     return kv_pool_fp4
 
 
@@ -404,9 +405,9 @@ def kv_dequantize_fp4(kv_pool_fp4, slots, kv=None, status=None, stream=None):
         with _made_on(stream, kv_pool_fp4.device):
             kv = torch.zeros((n, 576), dtype=torch.bfloat16, device=kv_pool_fp4.device)
     with _on(kv_pool_fp4, kv, slots, status):
-        _check(_lib.mla_kv_dequantize_fp4(_arg(kv_pool_fp4, "kv_pool_fp4", torch.uint8, nb, 64, FP4_ROW_BYTES),
-                                          _arg(slots, "slots", torch.int32, n), n, _arg(kv, "kv", torch.bfloat16, n, 576),
-                                          nb, _vec(status, "status", torch.int32), _stream(stream)),
+        _check(_lib.mla_kv_dequantize_fp4(_arg(kv_pool_fp4, "kv_pool_fp4", _U8, nb, 64, FP4_ROW_BYTES),
+                                          _arg(slots, "slots", _I32, n), n, _arg(kv, "kv", _BF16, n, 576),
+                                          nb, _vec(status, "status", _I32), _stream(stream)),
                "mla_kv_dequantize_fp4")
     return kv
 
@@ -487,8 +488,8 @@ def plan_device(dims: MlaDims, seq_lens, num_clusters: int, plan_dev=None, statu
         with _made_on(stream, seq_lens.device):
             plan_dev = torch.empty(_plan_words(dims.B * dims.s_q, num_clusters), dtype=torch.int32, device=seq_lens.device)
     with _on(seq_lens, plan_dev, status):
-        _check(_lib.mla_plan_device(ctypes.byref(dims), _arg(seq_lens, "seq_lens", torch.int32, dims.B), num_clusters,
-                                    _vec(plan_dev, "plan_dev", torch.int32), 4 * plan_dev.numel(), _vec(status, "status", torch.int32),
+        _check(_lib.mla_plan_device(ctypes.byref(dims), _arg(seq_lens, "seq_lens", _I32, dims.B), num_clusters,
+                                    _vec(plan_dev, "plan_dev", _I32), 4 * plan_dev.numel(), _vec(status, "status", _I32),
                                     _stream(stream)), "mla_plan_device")
     return plan_dev
 
@@ -506,9 +507,9 @@ def summarize_pages(kv_pool, blocks, codes, scales, kv_cache: str = "bf16", stat
     dtype, row = _POOL_ROWS[kv_cache]
     with _on(kv_pool, blocks, codes, scales, status):
         _check(_lib.mla_summarize_pages(_arg(kv_pool, "kv_pool", dtype, nb, 64, row), CACHE_KINDS[kv_cache],
-                                        _arg(blocks, "blocks", torch.int32, n), n, nb,
+                                        _arg(blocks, "blocks", _I32, n), n, nb,
                                         _arg(codes, "codes", torch.int8, nb, 576),
-                                        _arg(scales, "scales", torch.float32, nb), _vec(status, "status", torch.int32), _stream(stream)),
+                                        _arg(scales, "scales", _F32, nb), _vec(status, "status", _I32), _stream(stream)),
                "mla_summarize_pages")
     return codes, scales
 
@@ -526,12 +527,12 @@ def select_pages(dims: MlaDims, q_lat, q_rope, codes, scales, block_table, seq_l
     with _on(q_lat, q_rope, codes, scales, block_table, seq_lens, scores, sel_table, sel_lens, sel_pages, plan_dev,
              status):
         _check(_lib.mla_select_pages(
-            ctypes.byref(dims), _arg(q_lat, "q_lat", torch.bfloat16, N, H, 512),
-            _arg(q_rope, "q_rope", torch.bfloat16, N, H, 64), _arg(codes, "codes", torch.int8, dims.num_blocks, 576),
-            _arg(scales, "scales", torch.float32, dims.num_blocks),
+            ctypes.byref(dims), _arg(q_lat, "q_lat", _BF16, N, H, 512),
+            _arg(q_rope, "q_rope", _BF16, N, H, 64), _arg(codes, "codes", torch.int8, dims.num_blocks, 576),
+            _arg(scales, "scales", _F32, dims.num_blocks),
             _arg(block_table, "block_table", i32, dims.B, dims.max_blocks_per_seq),
             _arg(seq_lens, "seq_lens", i32, dims.B), k, n_first, n_recent,
-            _arg(scores, "scores", torch.float32, N, dims.max_blocks_per_seq), _arg(sel_table, "sel_table", i32, N, k),
+            _arg(scores, "scores", _F32, N, dims.max_blocks_per_seq), _arg(sel_table, "sel_table", i32, N, k),
             _arg(sel_lens, "sel_lens", i32, N), _arg(sel_pages, "sel_pages", i32, N, k), num_clusters,
             _vec(plan_dev, "plan_dev", i32), 0 if plan_dev is None else 4 * plan_dev.numel(),
             _vec(status, "status", i32), _stream(stream)), "mla_select_pages")
@@ -539,9 +540,9 @@ def select_pages(dims: MlaDims, q_lat, q_rope, codes, scales, block_table, seq_l
 
 
 def combine(dims, plan_dev, o_part, lse_part, o_lat, lse_out=None, stream=None, status=None):
-    plan_bytes, slots = _room(dims, 4096, plan_dev, o_part, lse_part)
-    _check(_lib.mla_combine_sized(ctypes.byref(dims), _ptr(plan_dev), plan_bytes, _ptr(o_part), _ptr(lse_part), slots,
-                                  _ptr(o_lat), _ptr(lse_out), _ptr(status), _stream(stream)), "mla_combine")
+    plan_bytes, o_bytes, lse_bytes = _sizes(dims, 4096, plan_dev, o_part, lse_part)
+    _check(_lib.mla_combine_sized(ctypes.byref(dims), _ptr(plan_dev), plan_bytes, _ptr(o_part), o_bytes, _ptr(lse_part),
+                                  lse_bytes, _ptr(o_lat), _ptr(lse_out), _ptr(status), _stream(stream)), "mla_combine")
 
 
 def qkv_a_proj(x, w_qkv_a, c_q=None, kv_a=None, stream=None):

@@ -469,21 +469,20 @@ mla_status_t mla_combine(const mla_dims_t* dims, const void* plan_dev, const flo
  * mla_decode_attn_sized, mla_combine_sized -- the attention (over the pool kind `cache`; draft_masks
  * as in mla_decode_attn_tree, bf16 cache only, or NULL) and the merge, with the sizes of the plan's
  * buffer and of the workspaces.  They are what a plan made on the device wants, whose slots
- * the host does not see: a plan that is longer than plan_bytes or splits rows into more
- * pieces than part_slots sets MLA_STATUS_BAD_PLAN and nothing is read or written through it.
- *   plan_bytes   size of plan_dev (a plan made by mla_plan or on the device fits mla_plan_size's)
- *   part_slots   slots that both hold: o_part part_slots x n_heads x 512 floats, lse_part
- *                part_slots x n_heads.  0: none, either may then be NULL (mla_combine_sized
- *                wants them all the same)
+ * the host does not see: a plan that is longer than its buffer or splits rows into more
+ * pieces than the workspaces hold sets MLA_STATUS_BAD_PLAN and nothing is read or written through it.
+ *   plan_bytes, o_part_bytes, lse_part_bytes   sizes of plan_dev, o_part and lse_part (mla_plan_size's
+ *                are enough for any plan; a slot takes n_heads x 512 floats of o_part and n_heads of
+ *                lse_part).  A workspace of 0 bytes may be NULL (not in mla_combine_sized)
  */
 mla_status_t mla_decode_attn_sized(const mla_dims_t* dims, int32_t cache, const void* q_lat, const void* q_rope,
                                    const void* kv_pool, const int32_t* block_table, const int32_t* seq_lens,
                                    const int32_t* draft_masks, const void* plan_dev, size_t plan_bytes,
-                                   int32_t num_clusters, float* o_part, float* lse_part, int32_t part_slots,
-                                   void* o_lat, float* lse_out, int32_t* status, void* stream);
+                                   int32_t num_clusters, float* o_part, size_t o_part_bytes, float* lse_part,
+                                   size_t lse_part_bytes, void* o_lat, float* lse_out, int32_t* status, void* stream);
 mla_status_t mla_combine_sized(const mla_dims_t* dims, const void* plan_dev, size_t plan_bytes, const float* o_part,
-                               const float* lse_part, int32_t part_slots, void* o_lat, float* lse_out,
-                               int32_t* status, void* stream);
+                               size_t o_part_bytes, const float* lse_part, size_t lse_part_bytes, void* o_lat,
+                               float* lse_out, int32_t* status, void* stream);
 
 /*
  * mla_decode_attn_combine_noalloc -- mla_decode_attn followed by mla_combine,

@@ -17,13 +17,13 @@ def refused(code, what, *args):
 
 
 def test_attention_arguments():
-    good = [ctypes.byref(D), 2, A, A, A, A, A, None, A, PLAN, 74, A, A, 76, A, None, None, None]
+    good = [ctypes.byref(D), 2, A, A, A, A, A, None, A, PLAN, 74, A, 76 * 16 * 2048, A, 76 * 64, A, None, None, None]
 
     def bad(i, v, code=1):
         args = list(good)
         args[i] = v
         refused(code, "mla_decode_attn_sized", *args)
-    for i in (2, 3, 4, 14):
+    for i in (2, 3, 4, 15):
         bad(i, None)
         bad(i, A + 8)
     for i in (5, 6, 8):
@@ -37,18 +37,17 @@ def test_attention_arguments():
     bad(10, 4097)
     bad(11, None)
     bad(11, A + 16)
-    bad(12, None)
-    bad(12, A + 2)
-    bad(13, -1)
-    bad(15, A + 2)
+    bad(13, None)
+    bad(13, A + 2)
     bad(16, A + 2)
+    bad(17, A + 2)
     args = list(good)
     args[1], args[7] = 0, A
     refused(1, "mla_decode_attn_sized", *args)      # masks with a causal plan
 
 
 def test_combine_arguments():
-    good = [ctypes.byref(D), A, PLAN, A, A, 76, A, None, None, None]
+    good = [ctypes.byref(D), A, PLAN, A, 76 * 16 * 2048, A, 76 * 64, A, None, None, None]
 
     def bad(i, v, code=1):
         args = list(good)
@@ -59,20 +58,20 @@ def test_combine_arguments():
     bad(2, 8, 3)
     bad(3, None)
     bad(3, A + 16)
-    bad(4, None)
-    bad(5, -1)
-    bad(6, None)
-    bad(7, A + 2)
+    bad(5, None)
+    bad(5, A + 2)
+    bad(7, None)
     bad(8, A + 2)
+    bad(9, A + 2)
 
 
-def test_room_of_tensors_and_addresses():
+def test_sizes_of_tensors_and_addresses():
     import torch
     plan = torch.zeros(100, dtype=torch.int32)
-    assert mla._room(D, 74, plan, torch.zeros(3 * 16 * 512), torch.zeros(5, 16)) == (400, 3)
-    assert mla._room(D, 74, plan, torch.zeros(3 * 16 * 512 - 1), torch.zeros(2, 16)) == (400, 2)
-    assert mla._room(D, 74, plan, None, torch.zeros(5, 16)) == (400, 0)
-    assert mla._room(D, 74, A, A, A) == (PLAN, 76)
+    assert mla._sizes(D, 74, plan, torch.zeros(3 * 16 * 512), torch.zeros(5, 16)) == (400, 3 * 16 * 2048, 320)
+    assert mla._sizes(D, 74, plan, None, torch.zeros(5, 16)) == (400, 0, 320)
+    assert mla._sizes(D, 74, A, A, A) == mla.plan_size(D, 74)
+    assert mla._sizes(D, 74, plan, A, None) == (400, mla.plan_size(D, 74)[1], 0)
 
 
 def test_a_tree_needs_its_masks():
