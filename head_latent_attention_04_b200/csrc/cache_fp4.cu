@@ -15,8 +15,10 @@
 // and 416 out per row (and the reverse).  A thread owns 8 columns (16 bytes of
 // bf16, 4 bytes of codes), 72 threads a row, so that every load and store of a
 // warp is contiguous; the four threads of a group combine their maxima by
-// shuffles.  16301 rows, from a graph: written in 7.0 us, read in 5.0 (3.9 us each at
-// the measured copy rate); 32 rows 1.4 and 1.6.  Reads go to L2 (__ldcg): the kernel before, whose end this one waits for
+// shuffles.  16301 rows, from a graph: written in 7.2 us, read in 5.0 (3.9 us each at
+// the measured copy rate); 65536 rows 25.6 and 22.2 (15.7 each); 32 rows 1.5 and 1.5.  The
+// writer's distance is no tail: a row's scales are sixteen 2-byte stores, and each
+// wave's first loads are exposed.  Reads go to L2 (__ldcg): the kernel before, whose end this one waits for
 // after its blocks have started, may have written what is read.
 #include "fp4_format.h"
 #include "mla_internal.h"
@@ -175,9 +177,9 @@ kv_dequantize_fp4_kernel(const uint8_t* pool, const int32_t* slots, long long n,
 
 // Rows per thread: one while the blocks of that are at most two per place on the card (a
 // step's rows: latency counts), else four (a prompt's: bytes in flight count).  One
-// against four, from a graph, writing / reading: 32 rows 1.6 / 1.6 against 2.5 / 2.4 us,
-// 4096 2.6 / 2.3 against 3.2 / 2.7, 8192 4.3 / 3.7 against 4.6 / 3.6, 16301 7.2 / 5.9
-// against 7.0 / 5.0, 65536 28 / 33 against 25 / 22.
+// against four, from a graph, writing / reading: 32 rows 1.5 / 1.5 against 2.5 / 2.2 us,
+// 4096 2.6 / 2.3 against 3.2 / 2.7, 8192 4.3 / 3.7 against 4.7 / 3.6, 16301 7.3 / 5.9
+// against 7.2 / 5.0, 65536 28.2 / 32.7 against 25.6 / 22.2.
 mla_status_t grid_of(long long n, bool* many, unsigned* blocks) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);

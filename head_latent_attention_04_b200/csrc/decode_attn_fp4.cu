@@ -9,18 +9,18 @@
 //
 // What bounds it.  A token is 416 bytes, so at 128 heads its 2 x 128 x 1088 operations
 // take 2.7 times as long at the measured tensor rate as its bytes at the measured copy
-// rate: the floor is the tensor cores' (4 x 128K tokens: 89 us).  The scales vary
-// along both products' reduction or output axes (a key's groups along q_lat . c_KV, keys along
-// P . c_KV), so no product can run on the 4-bit codes: every half page is
-// widened to fp16 in shared memory.  No unit is saturated (tensor pipe 34 %, issue
-// slots 47 %, shared memory 46 % on 32 x 4096 tokens): the kernel is bound by the
+// rate: the floor is the tensor cores' (4 x 128K tokens: 89 us).  The products do not run
+// on the 4-bit codes: q_lat and P stay in 16 bits and the scales are fp16, which no
+// block-scaled product takes, and along the keys, which P . c_KV sums over, the scales change with every
+// key.  So every half page is widened to fp16 in shared memory.  No unit is saturated (tensor pipe 32 %, issue
+// slots 46 %, shared memory 45 % on 32 x 4096 tokens): the kernel is bound by the
 // serial chains of its warps, and three of them turn once per 64-key page in about 2400 cycles
 // each, of which the tensor pipe needs 1088: the sender warps (two stages' waits,
 // widening 570, the scores' wait, conversion and store 700), the softmax warps (2500), and the exchange (a copy
 // takes 1050, the answer that the tile is free and the next copy's start as long again).
-// 4 x 128K tokens: 142 us launched from a graph, 165 us launched back to back for a second, where the
+// 4 x 128K tokens: 144.5 us launched from a graph, 165 us launched back to back for a second, where the
 // card's power limit holds the SM clock at 1.6 of 1.965 GHz; in that loop the bf16
-// cache's kernel takes 178 us, the FP8 cache's 186 (32 x 4096 tokens: 49 against 54
+// cache's kernel takes 179 us, the FP8 cache's 187 (32 x 4096 tokens: 48.5 against 54
 // and 57).  So the 4-bit cache holds 2.8 times the tokens of bf16 and is a little faster.
 //
 // Why this shape (as in decode_attn.cu).  O for 128 heads x 512 columns in fp32 is
@@ -55,7 +55,8 @@
 // when the own tile is free, their registers not live across that wait, 149; the wait for a P
 // buffer at the start of a page 148; a row's two softmax threads in one warp, joined by
 // a shuffle instead of a barrier, 145; eight sender warps 143.5, which read and free S before they wait
-// for the own tile 142.  Measured and not kept: a group of warps for the
+// for the own tile 142; scores added in fp32 and the stores into tensor memory behind their
+// fences, which is what they should compute and order, 144.5.  Measured and not kept: a group of warps for the
 // widening alone 144 to 181 us; two softmax groups taking pages in turn with one thread
 // per row 198; two tiles for the peer's scores (and three raw stages) 145; two or three barriers polled at once
 // 141.5 to 144; one wait for two barriers by different lanes 181 to 262; one lane waiting for its warp

@@ -5,8 +5,10 @@
 // kept in 8 bits: scale = amax / 127, code = rint(127 m / amax).  A query
 // row's heads are put in the same form, and the page's score is
 //   score = fp32( max_h ( (qcode_h . pcode) * qscale_h ) * pscale ):
-// the largest mean logit of any head, since all heads share the cache and a
-// page that one head needs is needed.  The first n_first and last n_recent
+// the largest mean logit of any head, since all heads share the pages.  It compares raw
+// logits: a head whose mean logits are high on every page outranks the others, although a
+// constant per head changes nothing in its softmax, and a page that only a head with small
+// logits needs may be left out.  The first n_first and last n_recent
 // pages of a query are always taken, then the best scores up to k pages, ties
 // to the lowest page.
 //
@@ -245,8 +247,8 @@ summarize_pages_kernel(const uint8_t* pool, const int32_t* blocks, int num_block
 // SMs) it is all latency: 7.9 us, of which 2.5 are dependent reads and the issue of the
 // copies, 3.4 the quantisation of 147 KB of queries, 1.1 the wait for the copies
 // and the product, 0.9 the maxima; where a block walks its row a further tile costs
-// 2.1 us, mostly waiting for its 74 KB.  With the selection behind it: 14.8 us for
-// 4 rows of 2048 pages, 28.2 for 122 rows of up to 1024.  The grid cuts a row into as many runs as fill the card.
+// 2.1 us, mostly waiting for its 74 KB.  With the selection behind it: 14.7 us for
+// 4 rows of 2048 pages, 28.4 for 122 rows of up to 1024.  The grid cuts a row into as many runs as fill the card.
 constexpr int kScoreThreads = 512;
 constexpr int kTile = 128;
 constexpr int kChunkBytes = kTile * 128;          // 128 rows x 128 K-bytes (SW128)

@@ -4,9 +4,10 @@
 // answers the host would otherwise compute and copy every step: what a step
 // costs is latency, so each job is one launch of one block of 1024 threads
 // with block-wide scans, and only a slot map of many tokens gets a second,
-// wide launch (bound by writing 8 bytes per token).  From a graph: tables 4.3 us and
-// plan 5.1 for 32 requests with one new token each; tables 16.0 us for 509 requests
-// with about a million new tokens, and the plan of their 1018 rows 9.8.
+// wide launch (bound by writing 8 bytes per token).  From a graph: tables 4.5 us and
+// plan 5.2 for 32 requests with one new token each; tables 16.1 us for 509 requests
+// with about a million new tokens (their 8500 page entries go through the one block),
+// and the plan of their 1018 rows 9.9.
 #include "block_scan.cuh"
 #include "mla_internal.h"
 #include "plan_device.cuh"
@@ -225,8 +226,8 @@ plan_kernel(const PlanShape p, const int32_t* seq_lens, int32_t* plan, int32_t* 
 
 // Slot maps up to this many tokens are written by the one block that makes the
 // tables (7 tokens per thread); longer ones by a launch of their own.  32 requests, from a
-// graph, in one block against two launches: 32 tokens 3.6 against 5.2 us, 2048
-// 5.4 against 9.3, 8192 9.7 against 8.9, 16384 15.6 against 7.9, 131072 96 against 7.7.
+// graph, in one block against two launches: 32 tokens 3.7 against 5.0 us, 2048
+// 5.5 against 9.7, 8192 9.7 against 8.1, 16384 15.5 against 7.9, 131072 93 against 7.7.
 constexpr int kOneBlockTokens = 7168;
 
 mla_status_t launch_build_tables(int B, const int32_t* cached_lens, const int32_t* new_lens, int max_blocks,

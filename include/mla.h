@@ -221,8 +221,10 @@ mla_status_t mla_plan(const mla_dims_t* dims, const int32_t* seq_lens_host, int3
  * mla_plan_size's slots).
  *
  * Numerics: the two CTAs of a cluster each score half of the 576 columns and
- * exchange their partial scores rounded to fp16; a partial of an attended key
- * beyond the fp16 range sets MLA_STATUS_SCORE_RANGE.  Cache rows past a row's
+ * exchange their partial scores rounded to fp16, which are added in fp16: with
+ * partials p0, p1 in log2 units a weight is off by a relative 2^-11 (|p0| + |p1| +
+ * |p0 + p1|) ln 2 at worst, and partials beyond the fp16 range are reported as
+ * MLA_STATUS_SCORE_RANGE says.  Cache rows past a row's
  * key count (page tails, other queries' keys) may hold anything, NaN and Inf
  * included: the kernel zeroes them in shared memory before the P.c_KV product.
  */
