@@ -331,8 +331,8 @@ def decode_attn_tree(dims, q_lat, q_rope, kv_pool, block_table, seq_lens, draft_
                      o_part, lse_part, o_lat, lse_out=None, status=None, stream=None):
     """decode_attn for drafts that form a tree: ``draft_masks`` int32 [B][s_q]
     (device), bit j of row i = draft j visible to query i (dims.causal must be 0)."""
-    if draft_masks is None:
-        raise ValueError("draft_masks is needed")
+    if draft_masks is None:         # without masks _decode_attn would run the causal kernel
+        raise MlaError(MLA_ERR_INVALID_ARG, "mla_decode_attn_tree: draft_masks is None")
     _decode_attn("mla_decode_attn_tree", "bf16", dims, q_lat, q_rope, kv_pool, block_table, seq_lens, draft_masks,
                  plan_dev, num_clusters, o_part, lse_part, o_lat, lse_out, status, stream)
 

@@ -75,5 +75,5 @@ def test_sizes_of_tensors_and_addresses():
 
 
 def test_a_tree_needs_its_masks():
-    with pytest.raises(ValueError, match="draft_masks"):
+    with pytest.raises(mla.MlaError, match="draft_masks"):
         mla.decode_attn_tree(D, A, A, A, A, A, None, A, 74, None, None, A)
